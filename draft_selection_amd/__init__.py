@@ -20,6 +20,14 @@ Entry points (same names as the C ABI):
   verify(target_logits, cand_id, path_slot, ...)    -> n_accepted, out_tok
   dyn_conv(x, x_prev, base, W_c)                    -> y
   lmhead_topk(h, W)                                 -> cand_id, cand_u
+  tree_mask(parent)                                 -> mask, depth
+  tree_attn(q, k_cache, v_cache, page_table, seq_len, mask) -> out, lse
+  tree_accept(parent, tok, target_tok)              -> n_keep, path, out_tok
+  cache_append(k_new, v_new, k_cache, v_cache, page_table, seq_len)
+  cache_compact(k_cache, v_cache, page_table, seq_len, path, n_keep) -> new_len
+  pages_reserve(pages, extra), pages_fork(pages, src, k_cache, v_cache)
+                                                    -> granted
+  pages_free(pages, which)                          (pages: a Pages tuple)
   device_error()                                    -> sticky device error bits
 Every batch call takes ``block_len`` (a ragged batch: valid positions per
 block, int32 on the GPU) and ``stream``.
@@ -30,7 +38,7 @@ import ctypes as C
 import functools
 import inspect
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -39,7 +47,9 @@ LIB_PATH = os.path.join(_PKG, "libdsel.so")
 K = 16
 MAX_BLOCK = 32
 GREEDY, SAMPLED = 0, 1
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
+MAX_TREE = 256
+DEVERR_TOKEN_RANGE, DEVERR_BLOCK_LEN, DEVERR_SEQ_LEN, DEVERR_PAGE, DEVERR_TREE, DEVERR_POOL = 1, 2, 4, 8, 16, 32
 
 _STATUS = {0: "DSEL_OK", -1: "DSEL_E_ARG", -2: "DSEL_E_DTYPE", -3: "DSEL_E_ALIGN",
            -4: "DSEL_E_WORKSPACE", -5: "DSEL_E_HIP"}
@@ -64,6 +74,27 @@ class PathArgs(C.Structure):
                 ("batch", C.c_int64), ("block", C.c_int64), ("block_len", C.c_void_p),
                 ("cand_id", C.c_void_p), ("cand_u", C.c_void_p), ("A_prev", C.c_void_p), ("B_cur", C.c_void_p),
                 ("G", C.c_void_p), ("S", C.c_void_p)]
+
+
+class CacheArgs(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("dt", C.c_int32), ("layers", C.c_int64),
+                ("layer_stride", C.c_int64), ("num_pages", C.c_int64), ("page_stride", C.c_int64),
+                ("page_size", C.c_int64), ("slot_stride", C.c_int64), ("heads", C.c_int64),
+                ("head_stride", C.c_int64), ("dim", C.c_int64), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p)]
+
+
+class TreeAttnArgs(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("q_batch", C.c_int64), ("q_token", C.c_int64), ("q_head", C.c_int64),
+                ("batch", C.c_int64), ("block", C.c_int64), ("q_heads", C.c_int64), ("block_len", C.c_void_p),
+                ("page_table", C.c_void_p), ("table_ld", C.c_int64), ("max_pages", C.c_int64),
+                ("seq_len", C.c_void_p), ("mask", C.c_void_p), ("scale", C.c_float), ("out", C.c_void_p),
+                ("lse", C.c_void_p)]
+
+
+class PagesArgs(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("table_ld", C.c_int64), ("rows", C.c_int64), ("max_pages", C.c_int64),
+                ("row_pages", C.c_void_p), ("seq_len", C.c_void_p), ("refcount", C.c_void_p),
+                ("num_pages", C.c_int64), ("page_size", C.c_int64)]
 
 
 _lib = None
@@ -102,6 +133,16 @@ def _load():
             "dsel_lmhead_topk": ([P, P, I64, I64, I64, P, P, P, SZ, P], I32),
             "dsel_dyn_conv": ([P, P, P, P, I64, I64, P, I64, P, P, SZ, P], I32),
             "dsel_verify": ([P, I32, I64, I64, P, I64, I64, P, P, P, I32, C.c_float, P, P, P, P, P, SZ, P], I32),
+            "dsel_tree_mask": ([P, I64, I64, P, P, P, P], I32),
+            "dsel_tree_attn_workspace_bytes": ([I64, I64, I64, I64, I64], SZ),
+            "dsel_tree_attn": ([C.POINTER(TreeAttnArgs), C.POINTER(CacheArgs), P, SZ, P], I32),
+            "dsel_tree_accept": ([P, P, P, I64, I64, I64, P, P, P, P, P], I32),
+            "dsel_cache_append": ([P, P, C.POINTER(I64), C.POINTER(CacheArgs), P, I64, I64, P, I64, I64, P, P], I32),
+            "dsel_cache_compact": ([C.POINTER(CacheArgs), P, I64, I64, P, P, P, I64, I64, P, P], I32),
+            "dsel_pages_reserve": ([C.POINTER(PagesArgs), P, P, P], I32),
+            "dsel_pages_fork_workspace_bytes": ([I64], SZ),
+            "dsel_pages_fork": ([C.POINTER(PagesArgs), P, C.POINTER(CacheArgs), P, P, SZ, P], I32),
+            "dsel_pages_free": ([C.POINTER(PagesArgs), P, P], I32),
             "dsel_device_error": ([C.POINTER(C.c_int32), P], I32),
             "dsel_status_string": ([I32], C.c_char_p),
             "dsel_version": ([], I32),
@@ -664,3 +705,299 @@ def select_path_route(batch: int, block: int, vocab: int, dtype, d: int, r: int,
     pa = PathArgs(None, dt, vocab, vocab, None, d, None, None, None, r, None, None, batch, block, None, None, None,
                   mark, mark, mark, None)
     return int(_load().dsel_select_path_route(C.byref(pa)))
+
+
+# ---- the cache side of verifying drafted tokens ---------------------------------
+
+
+class Pages(NamedTuple):
+    """The pool of pages behind a table of rows (dsel_pages): ``table [rows,
+    max_pages]``, ``row_pages [rows]``, ``seq_len [rows]`` and ``refcount
+    [num_pages]`` (0 = free), all int32 on the GPU and updated in place."""
+    table: torch.Tensor
+    row_pages: torch.Tensor
+    seq_len: torch.Tensor
+    refcount: torch.Tensor
+    page_size: int
+
+
+def _placed(fn):
+    """Run ``fn`` on its first argument's device and on ``stream`` (default: that
+    device's current stream), both made current, so that what it allocates
+    belongs to the stream its kernels are launched on."""
+
+    @functools.wraps(fn)
+    def wrap(first, *args, stream=None, **kwargs):
+        t = first.table if isinstance(first, Pages) else first
+        if not t.is_cuda:
+            raise ValueError(f"{fn.__name__}: the tensors must be on the GPU")
+        if stream is not None:
+            if stream.device != t.device:
+                raise ValueError(f"{fn.__name__}: stream is of {stream.device}, the tensors are on {t.device}")
+            with torch.cuda.stream(stream):
+                return fn(first, *args, **kwargs)
+        if t.device.index != torch.cuda.current_device():
+            with torch.cuda.device(t.device):
+                return fn(first, *args, **kwargs)
+        return fn(first, *args, **kwargs)
+
+    return wrap
+
+
+def _on(dev, t, name, dtype, shape=None):
+    _need(t, name, dtype, shape)
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _lens_on(dev, block_len, B):
+    if block_len is None:
+        return None
+    _on(dev, block_len, "block_len", torch.int32, (B,))
+    return block_len.data_ptr()
+
+
+def _table(dev, page_table, seq_len, B):
+    """Checked ``(row stride, pages per row)`` of a page table ``[B, max_pages]``
+    with unit stride inside a row."""
+    if page_table.device != dev or page_table.dtype != torch.int32:
+        raise TypeError(f"page_table must be int32 on {dev}")
+    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.shape[1] < 1:
+        raise ValueError(f"page_table must be [{B}, max_pages]")
+    n = page_table.shape[1]
+    ld = page_table.stride(0) if B > 1 else n
+    if (n > 1 and page_table.stride(1) != 1) or ld < n:
+        raise ValueError("page_table must have unit stride in its rows")
+    _on(dev, seq_len, "seq_len", torch.int32, (B,))
+    return ld, n
+
+
+def _cache(dev, k, v, k_scale=None, v_scale=None) -> CacheArgs:
+    """Arguments of a cache ``[num_pages, page_size, heads, dim]`` or ``[layers,
+    num_pages, page_size, heads, dim]``: any strides (the same for K and V), the
+    last one 1."""
+    if k.shape != v.shape or k.dim() not in (4, 5):
+        raise ValueError("k_cache and v_cache must be [layers,] [num_pages, page_size, heads, dim] alike")
+    if k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError("k_cache and v_cache must both be bfloat16 or float8_e4m3fn")
+    if k.device != dev or v.device != dev:
+        raise ValueError(f"the caches must be on {dev}")
+    shape, sk, sv = k.shape, k.stride(), v.stride()
+    if sk[-1] != 1 or sv[-1] != 1:
+        raise ValueError("the caches need unit stride in the last dim")
+    if sk != sv and any(n > 1 and a != b for n, a, b in zip(shape, sk, sv)):
+        raise ValueError("k_cache and v_cache must have the same strides")
+    if k.dim() == 4:
+        shape, sk = (1,) + tuple(shape), (0,) + tuple(sk)
+    L, N, P, H, D = shape
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t is None:
+            continue
+        if k.dtype != torch.float8_e4m3fn:
+            raise ValueError(f"{n} is for float8_e4m3fn caches")
+        _on(dev, t, n, torch.float32, (H,) if k.dim() == 4 else (L, H))
+    return CacheArgs(k.data_ptr(), v.data_ptr(), BF16 if k.dtype == torch.bfloat16 else E4M3, L, sk[0], N, sk[1], P,
+                     sk[2], H, sk[3], D, k_scale.data_ptr() if k_scale is not None else None,
+                     v_scale.data_ptr() if v_scale is not None else None)
+
+
+def _cur():
+    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+@_placed
+def tree_mask(parent, block_len=None, out=None):
+    """Which nodes of a drafted tree each node sees, and its depth: ``parent [B,
+    T]`` int32 (-1 at node 0, the last verified token; below the node's own index
+    elsewhere).  Returns ``mask [B, T, ceil(T / 32)]`` int32 (bit ``j % 32`` of
+    word ``j / 32``: the node itself and the nodes above it) and ``depth [B, T]``
+    int32.  Nodes past ``block_len`` are not written."""
+    B, T = parent.shape
+    dev = parent.device
+    _on(dev, parent, "parent", torch.int32)
+    if out is None:
+        mask = torch.empty((B, T, (T + 31) // 32), dtype=torch.int32, device=dev)
+        depth = torch.empty((B, T), dtype=torch.int32, device=dev)
+    else:
+        mask, depth = out
+        _on(dev, mask, "mask", torch.int32, (B, T, (T + 31) // 32))
+        _on(dev, depth, "depth", torch.int32, (B, T))
+    _check(_load().dsel_tree_mask(parent.data_ptr(), B, T, _lens_on(dev, block_len, B), mask.data_ptr(),
+                                  depth.data_ptr(), _cur()), "dsel_tree_mask")
+    return mask, depth
+
+
+def tree_attn_workspace_bytes(batch: int, block: int, q_heads: int, kv_heads: int, dim: int) -> int:
+    return int(_load().dsel_tree_attn_workspace_bytes(batch, block, q_heads, kv_heads, dim))
+
+
+@_placed
+def tree_attn(q, k_cache, v_cache, page_table, seq_len, mask=None, block_len=None, scale=None, k_scale=None,
+              v_scale=None, out=None, lse=None, want_lse=False, workspace=None):
+    """Attention of drafted tokens over one layer of a paged cache and each other.
+
+    ``q [B, T, q_heads, dim]`` bf16 (any strides, the last one 1), caches
+    ``[num_pages, page_size, heads, dim]`` bf16 or float8_e4m3fn (any strides, the
+    last one 1; ``k_scale``, ``v_scale [heads]`` fp32 for the latter),
+    ``page_table [B, max_pages]``, ``seq_len [B]`` int32.  K and V of the tokens
+    are in the cache, at positions ``seq_len[b] + t``.  Every token sees the
+    ``seq_len`` cached positions, and the tokens whose bits are set in its row of
+    ``mask`` (tree_mask's layout; None: those up to itself).  ``scale`` defaults
+    to ``dim ** -0.5``.  Returns ``(out [B, T, q_heads, dim] bf16, lse [B, T,
+    q_heads] fp32 or None)``; a token that sees nothing gets 0 and -inf."""
+    if q.dim() != 4 or q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16 [B, T, q_heads, dim]")
+    B, T, Hq, D = q.shape
+    dev = q.device
+    if q.stride(3) != 1 and D > 1:
+        raise ValueError("q must have unit stride in the last dim")
+    if k_cache.dim() != 4:
+        raise ValueError("tree_attn takes one layer's cache [num_pages, page_size, heads, dim]")
+    c = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    if c.dim != D:
+        raise ValueError(f"q has head dim {D}, the cache {c.dim}")
+    ld, n = _table(dev, page_table, seq_len, B)
+    if mask is not None:
+        _on(dev, mask, "mask", torch.int32, (B, T, (T + 31) // 32))
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _on(dev, out, "out", torch.bfloat16, (B, T, Hq, D))
+    if lse is not None:
+        _on(dev, lse, "lse", torch.float32, (B, T, Hq))
+    elif want_lse:
+        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev)
+    need = tree_attn_workspace_bytes(B, T, Hq, c.heads, D)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {dev}")
+    sq = q.stride()
+    a = TreeAttnArgs(q.data_ptr(), sq[0], sq[1], sq[2], B, T, Hq, _lens_on(dev, block_len, B), page_table.data_ptr(),
+                     ld, n, seq_len.data_ptr(), mask.data_ptr() if mask is not None else None,
+                     float(D ** -0.5 if scale is None else scale), out.data_ptr(),
+                     lse.data_ptr() if lse is not None else None)
+    _check(_load().dsel_tree_attn(C.byref(a), C.byref(c), workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _cur()), "dsel_tree_attn")
+    return out, lse
+
+
+@_placed
+def tree_accept(parent, tok, target_tok, block_len=None):
+    """The path of a tree that the target keeps: from node 0, the lowest child
+    whose ``tok`` is the target's token after the current node, while there is
+    one.  ``parent``, ``tok [B, T]`` int32; ``target_tok [B, T]`` int32 of evenly
+    spaced elements (``cand_id[:, :, 0]`` of select_topk on the target's logits is
+    greedy verification).  Returns ``n_keep [B]`` (kept nodes, the verified one
+    included), ``path [B, T]`` (their indices, -1 behind) and ``out_tok [B, T]``
+    (the accepted tokens and the target's own next one, -1 behind)."""
+    B, T = parent.shape
+    dev = parent.device
+    _on(dev, parent, "parent", torch.int32)
+    _on(dev, tok, "tok", torch.int32, (B, T))
+    if target_tok.dtype != torch.int32 or target_tok.device != dev or tuple(target_tok.shape) != (B, T):
+        raise TypeError(f"target_tok must be int32 [{B}, {T}] on {dev}")
+    step = target_tok.stride(1) if T > 1 else target_tok.stride(0) if B > 1 else 1
+    if step < 1 or (B > 1 and target_tok.stride(0) != T * step):
+        raise ValueError("target_tok must be evenly spaced")
+    n_keep = torch.empty(B, dtype=torch.int32, device=dev)
+    path = torch.empty((B, T), dtype=torch.int32, device=dev)
+    out_tok = torch.empty((B, T), dtype=torch.int32, device=dev)
+    _check(_load().dsel_tree_accept(parent.data_ptr(), tok.data_ptr(), target_tok.data_ptr(), step, B, T,
+                                    _lens_on(dev, block_len, B), n_keep.data_ptr(), path.data_ptr(),
+                                    out_tok.data_ptr(), _cur()), "dsel_tree_accept")
+    return n_keep, path, out_tok
+
+
+@_placed
+def cache_append(k_new, v_new, k_cache, v_cache, page_table, seq_len, block_len=None, k_scale=None, v_scale=None):
+    """K and V of new tokens written behind the cached ones (positions
+    ``seq_len[b] + t``): ``k_new``, ``v_new [B, T, heads, dim]`` bf16 for a cache of
+    one layer, ``[layers, B, T, heads, dim]`` for one of several (any strides, the
+    same for both, the last one 1).  float8_e4m3fn caches take ``x / scale``, held
+    to +-448.  ``seq_len`` is not changed."""
+    dev = k_new.device
+    c = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    if k_new.dim() != k_cache.dim() or k_new.shape != v_new.shape:
+        raise ValueError("k_new and v_new must be [layers,] [B, T, heads, dim] as the cache")
+    if k_new.dtype != torch.bfloat16 or v_new.dtype != torch.bfloat16:
+        raise TypeError("k_new and v_new must be bfloat16")
+    if v_new.device != dev:
+        raise ValueError(f"v_new is on {v_new.device}, expected {dev}")
+    shape, sk, sv = k_new.shape, k_new.stride(), v_new.stride()
+    if sk[-1] != 1 or sv[-1] != 1 or (sk != sv and any(n > 1 and a != b for n, a, b in zip(shape, sk, sv))):
+        raise ValueError("k_new and v_new must have the same strides, the last one 1")
+    if len(shape) == 4:
+        shape, sk = (1,) + tuple(shape), (0,) + tuple(sk)
+    L, B, T, H, D = shape
+    if (L, H, D) != (c.layers, c.heads, c.dim):
+        raise ValueError(f"new rows of {(L, H, D)} (layers, heads, dim), the cache has {(c.layers, c.heads, c.dim)}")
+    ld, n = _table(dev, page_table, seq_len, B)
+    _check(_load().dsel_cache_append(k_new.data_ptr(), v_new.data_ptr(), (C.c_int64 * 4)(*sk[:4]), C.byref(c),
+                                     page_table.data_ptr(), ld, n, seq_len.data_ptr(), B, T,
+                                     _lens_on(dev, block_len, B), _cur()), "dsel_cache_append")
+
+
+@_placed
+def cache_compact(k_cache, v_cache, page_table, seq_len, path, n_keep, new_len=None):
+    """Keeps a path of the appended tokens: in every layer the rows at ``seq_len[b]
+    + path[b, i]`` move to ``seq_len[b] + i`` for ``i < n_keep[b]`` (path ascends, as
+    tree_accept gives it).  Returns ``new_len [B]`` int32, the rows' new lengths."""
+    dev = k_cache.device
+    c = _cache(dev, k_cache, v_cache)
+    B, T = path.shape
+    _on(dev, path, "path", torch.int32)
+    _on(dev, n_keep, "n_keep", torch.int32, (B,))
+    ld, n = _table(dev, page_table, seq_len, B)
+    if new_len is None:
+        new_len = torch.empty(B, dtype=torch.int32, device=dev)
+    _on(dev, new_len, "new_len", torch.int32, (B,))
+    _check(_load().dsel_cache_compact(C.byref(c), page_table.data_ptr(), ld, n, seq_len.data_ptr(), path.data_ptr(),
+                                      n_keep.data_ptr(), B, T, new_len.data_ptr(), _cur()), "dsel_cache_compact")
+    return new_len
+
+
+def _pages(p: Pages, arg, name) -> PagesArgs:
+    dev = p.table.device
+    R = p.table.shape[0]
+    ld, n = _table(dev, p.table, p.seq_len, R)
+    _on(dev, p.row_pages, "row_pages", torch.int32, (R,))
+    _on(dev, p.refcount, "refcount", torch.int32)
+    _on(dev, arg, name, torch.int32, (R,))
+    return PagesArgs(p.table.data_ptr(), ld, R, n, p.row_pages.data_ptr(), p.seq_len.data_ptr(),
+                     p.refcount.data_ptr(), p.refcount.numel(), p.page_size)
+
+
+@_placed
+def pages_reserve(pages: Pages, extra):
+    """Gives every row the pages it lacks to hold ``seq_len[r] + extra[r]``
+    positions: the lowest free ones, in row order; all rows or none.  Returns
+    ``granted [1]`` int32 (0 also sets DEVERR_POOL)."""
+    a = _pages(pages, extra, "extra")
+    granted = torch.ones(1, dtype=torch.int32, device=extra.device) if a.rows == 0 else \
+        torch.empty(1, dtype=torch.int32, device=extra.device)
+    _check(_load().dsel_pages_reserve(C.byref(a), extra.data_ptr(), granted.data_ptr(), _cur()), "dsel_pages_reserve")
+    return granted
+
+
+@_placed
+def pages_fork(pages: Pages, src, k_cache, v_cache):
+    """Row r becomes a copy of row ``src[r]`` (-1: takes no part): whole pages
+    shared, the partial last one copied in every layer; all rows or none.  Row r
+    must hold no page.  Returns ``granted [1]`` int32."""
+    a = _pages(pages, src, "src")
+    dev = src.device
+    c = _cache(dev, k_cache, v_cache)
+    granted = torch.ones(1, dtype=torch.int32, device=dev) if a.rows == 0 else \
+        torch.empty(1, dtype=torch.int32, device=dev)
+    ws = torch.empty(max(a.rows, 1), dtype=torch.int32, device=dev)
+    _check(_load().dsel_pages_fork(C.byref(a), src.data_ptr(), C.byref(c), granted.data_ptr(), ws.data_ptr(),
+                                   ws.numel() * 4, _cur()), "dsel_pages_fork")
+    return granted
+
+
+@_placed
+def pages_free(pages: Pages, which):
+    """Rows with ``which[r] != 0`` give back every page they hold."""
+    a = _pages(pages, which, "which")
+    _check(_load().dsel_pages_free(C.byref(a), which.data_ptr(), _cur()), "dsel_pages_free")

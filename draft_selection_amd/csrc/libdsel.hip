@@ -18,6 +18,8 @@
 #include "path.h"
 #include "project.h"
 #include "topk16.h"
+#include "tree.h"
+#include "treeattn.h"
 #include "verify.h"
 
 #define DSEL_API extern "C" __attribute__((visibility("default")))
@@ -1121,6 +1123,302 @@ DSEL_API dsel_status dsel_dyn_conv(const uint16_t *x, const uint16_t *x_prev, co
     if (st != DSEL_OK) return st;
     return launch((const void *)conv_apply_kernel, dim3((unsigned)p.M), dim3(256), &p,
                   (size_t)p.N * sizeof(float), stream);
+}
+
+// ---- the cache side of verifying a tree ---------------------------------------
+
+namespace {
+
+// Checks a cache and lays its strides out in 16-byte vectors.  A stride of an
+// extent of one is never used and may be anything.  `data` false: only the
+// page geometry is used, and K, V may be missing.
+dsel_status check_cache(const dsel_cache *c, CacheView *v) {
+    if (!c) return DSEL_E_ARG;
+    if (c->dt != DSEL_BF16 && c->dt != DSEL_E4M3) return DSEL_E_DTYPE;
+    const int64_t es = c->dt == DSEL_BF16 ? 2 : 1, per = 16 / es;
+    if (c->layers < 1 || c->layers > DSEL_MAX_LAYERS || c->heads < 1 || c->heads > DSEL_MAX_HEADS || c->dim < 1 ||
+        c->dim > DSEL_MAX_HEAD_DIM || c->num_pages < 1 || c->num_pages > INT_MAX || c->page_size < 1 ||
+        c->page_size > DSEL_MAX_PAGE)
+        return DSEL_E_ARG;
+    if (!c->k || !c->v) return DSEL_E_ARG;
+    if (c->dt == DSEL_BF16 && (c->k_scale || c->v_scale)) return DSEL_E_ARG;
+    if (c->dim % per || !aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+        return DSEL_E_ALIGN;
+    const int64_t extent[4] = {c->layers, c->num_pages, c->page_size, c->heads};
+    const int64_t stride[4] = {c->layer_stride, c->page_stride, c->slot_stride, c->head_stride};
+    int64_t st[4], reach = 0;
+    for (int i = 0; i < 4; ++i) {
+        st[i] = 0;
+        if (extent[i] == 1) continue;
+        if (stride[i] < c->dim || stride[i] > (INT64_MAX / 4 - reach) / extent[i]) return DSEL_E_ARG;
+        if (stride[i] % per) return DSEL_E_ALIGN;
+        st[i] = stride[i] / per;
+        reach += stride[i] * (extent[i] - 1);
+    }
+    v->k = (char *)c->k;
+    v->v = (char *)c->v;
+    v->layers = (int)c->layers;
+    v->heads = (int)c->heads;
+    v->vecs = (int)(c->dim / per);
+    v->layer_stride = st[0];
+    v->page_stride = st[1];
+    v->slot_stride = st[2];
+    v->head_stride = st[3];
+    v->num_pages = c->num_pages;
+    v->page_size = (int)c->page_size;
+    v->k_scale = c->k_scale;
+    v->v_scale = c->v_scale;
+    return DSEL_OK;
+}
+
+// The batch that reads or writes a cache through its page table
+dsel_status check_table(const int32_t *table, int64_t ld, int64_t max_pages, int64_t page_size,
+                        const int32_t *seq_len, int64_t batch, int64_t block, const int32_t *block_len,
+                        TableView *t) {
+    if (max_pages < 1 || ld < max_pages || max_pages > (INT_MAX - DSEL_MAX_PAGE) / page_size ||
+        ld > INT64_MAX / 8 / (batch + 1))
+        return DSEL_E_ARG;
+    if (batch == 0 || block == 0) return DSEL_OK;
+    if (!table || !seq_len) return DSEL_E_ARG;
+    if (!aligned(table, 4) || !aligned(seq_len, 4) || !aligned(block_len, 4)) return DSEL_E_ALIGN;
+    t->table = table;
+    t->ld = ld;
+    t->max_pages = (int)max_pages;
+    t->seq_len = seq_len;
+    return DSEL_OK;
+}
+
+dsel_status check_tree(int64_t batch, int64_t block) {
+    return batch < 0 || batch > DSEL_MAX_TREE_BATCH || block < 1 || block > DSEL_MAX_TREE ? DSEL_E_ARG : DSEL_OK;
+}
+
+}  // namespace
+
+DSEL_API dsel_status dsel_tree_mask(const int32_t *parent, int64_t batch, int64_t block, const int32_t *block_len,
+                                    int32_t *mask, int32_t *depth, dsel_stream_t stream) {
+    dsel_status st = check_tree(batch, block);
+    if (st != DSEL_OK) return st;
+    if (batch == 0) return DSEL_OK;
+    if (!parent || !mask) return DSEL_E_ARG;
+    if (!aligned(parent, 4) || !aligned(mask, 4) || !aligned(depth, 4) || !aligned(block_len, 4)) return DSEL_E_ALIGN;
+    TreeParams p{};
+    p.parent = parent;
+    p.T = (int)block;
+    p.len = block_len;
+    p.mask = mask;
+    p.depth = depth;
+    return launch((const void *)tree_mask_kernel, dim3((unsigned)batch), dim3((unsigned)(block + 63) / 64 * 64), &p, 0,
+                  stream);
+}
+
+DSEL_API dsel_status dsel_tree_accept(const int32_t *parent, const int32_t *tok, const int32_t *target_tok,
+                                      int64_t target_stride, int64_t batch, int64_t block, const int32_t *block_len,
+                                      int32_t *n_keep, int32_t *path, int32_t *out_tok, dsel_stream_t stream) {
+    dsel_status st = check_tree(batch, block);
+    if (st != DSEL_OK) return st;
+    if (target_stride < 1 || target_stride > (1 << 30)) return DSEL_E_ARG;
+    if (batch == 0) return DSEL_OK;
+    if (!parent || !tok || !target_tok || !n_keep || !path || !out_tok) return DSEL_E_ARG;
+    if (!aligned(parent, 4) || !aligned(tok, 4) || !aligned(target_tok, 4) || !aligned(n_keep, 4) ||
+        !aligned(path, 4) || !aligned(out_tok, 4) || !aligned(block_len, 4))
+        return DSEL_E_ALIGN;
+    TreeParams p{};
+    p.parent = parent;
+    p.tok = tok;
+    p.target = target_tok;
+    p.target_stride = target_stride;
+    p.T = (int)block;
+    p.len = block_len;
+    p.n_keep = n_keep;
+    p.path = path;
+    p.out_tok = out_tok;
+    return launch((const void *)tree_accept_kernel, dim3((unsigned)batch), dim3(64), &p, 0, stream);
+}
+
+DSEL_API size_t dsel_tree_attn_workspace_bytes(int64_t batch, int64_t block, int64_t q_heads, int64_t kv_heads,
+                                               int64_t dim) {
+    (void)batch, (void)block, (void)q_heads, (void)kv_heads, (void)dim;
+    return 0;
+}
+
+DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cache *cache, void *workspace,
+                                    size_t workspace_bytes, dsel_stream_t stream) {
+    if (!a) return DSEL_E_ARG;
+    dsel_status st = check_tree(a->batch, a->block);
+    if (st != DSEL_OK) return st;
+    TreeAttnParams p{};
+    if ((st = check_cache(cache, &p.c)) != DSEL_OK) return st;
+    if (cache->layers != 1 || a->q_heads < 1 || a->q_heads > DSEL_MAX_HEADS || a->q_heads % cache->heads)
+        return DSEL_E_ARG;
+    if (!(a->scale > 0.0f && a->scale < __builtin_inff())) return DSEL_E_ARG;
+    if ((st = check_table(a->page_table, a->table_ld, a->max_pages, cache->page_size, a->seq_len, a->batch, a->block,
+                          a->block_len, &p.t)) != DSEL_OK)
+        return st;
+    if (a->batch == 0) return DSEL_OK;
+    if (!a->q || !a->out) return DSEL_E_ARG;
+    if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->lse, 4) || !aligned(a->mask, 4)) return DSEL_E_ALIGN;
+    const int64_t extent[3] = {a->batch, a->block, a->q_heads}, stride[3] = {a->q_batch, a->q_token, a->q_head};
+    int64_t sq[3];
+    for (int i = 0; i < 3; ++i) {
+        sq[i] = 0;
+        if (extent[i] == 1) continue;
+        if (stride[i] < 0 || stride[i] > INT64_MAX / 16 / extent[i]) return DSEL_E_ARG;
+        if (stride[i] % 8) return DSEL_E_ALIGN;
+        sq[i] = stride[i];
+    }
+    if (workspace_bytes < dsel_tree_attn_workspace_bytes(a->batch, a->block, a->q_heads, cache->heads, cache->dim))
+        return DSEL_E_WORKSPACE;
+    p.q = (const char *)a->q;
+    p.sqb = sq[0];
+    p.sqt = sq[1];
+    p.sqh = sq[2];
+    p.out = a->out;
+    p.lse = a->lse;
+    p.mask = a->mask;
+    p.len = a->block_len;
+    p.B = (int)a->batch;
+    p.T = (int)a->block;
+    p.Hq = (int)a->q_heads;
+    p.D = (int)cache->dim;
+    p.group = (int)(a->q_heads / cache->heads);
+    p.words = (int)(a->block + 31) / 32;
+    p.scale = (float)((double)a->scale * 1.4426950408889634);
+    const void *k = cache->dt == DSEL_E4M3 ? (const void *)tree_attn_simple_kernel<true>
+                                           : (const void *)tree_attn_simple_kernel<false>;
+    return launch(k, dim3((unsigned)p.Hq, (unsigned)p.T, (unsigned)p.B), dim3(64), &p, 0, stream);
+}
+
+DSEL_API dsel_status dsel_cache_append(const uint16_t *k_new, const uint16_t *v_new, const int64_t strides[4],
+                                       const dsel_cache *cache, const int32_t *page_table, int64_t table_ld,
+                                       int64_t max_pages, const int32_t *seq_len, int64_t batch, int64_t block,
+                                       const int32_t *block_len, dsel_stream_t stream) {
+    if (batch < 0 || batch > DSEL_MAX_TREE_BATCH || block < 0 || block > INT_MAX / 2) return DSEL_E_ARG;
+    AppendParams p{};
+    dsel_status st = check_cache(cache, &p.c);
+    if (st != DSEL_OK) return st;
+    if ((st = check_table(page_table, table_ld, max_pages, cache->page_size, seq_len, batch, block, block_len, &p.t)) !=
+        DSEL_OK)
+        return st;
+    if (batch == 0 || block == 0) return DSEL_OK;
+    if (!k_new || !v_new || !strides) return DSEL_E_ARG;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16)) return DSEL_E_ALIGN;
+    const int64_t extent[4] = {cache->layers, batch, block, cache->heads};
+    int64_t sn[4];
+    for (int i = 0; i < 4; ++i) {
+        sn[i] = 0;
+        if (extent[i] == 1) continue;
+        if (strides[i] < 0 || strides[i] > INT64_MAX / 16 / extent[i]) return DSEL_E_ARG;
+        if (strides[i] % 8) return DSEL_E_ALIGN;
+        sn[i] = strides[i] / 8;
+    }
+    p.k = (const char *)k_new;
+    p.v = (const char *)v_new;
+    p.sl = sn[0];
+    p.sb = sn[1];
+    p.st = sn[2];
+    p.sh = sn[3];
+    p.T = (int)block;
+    p.len = block_len;
+    const void *k = cache->dt == DSEL_E4M3 ? (const void *)cache_append_kernel<true>
+                                           : (const void *)cache_append_kernel<false>;
+    return launch(k, dim3((unsigned)((block + kAppendTokens - 1) / kAppendTokens), (unsigned)cache->layers * 2,
+                          (unsigned)batch), dim3(256), &p, 0, stream);
+}
+
+DSEL_API dsel_status dsel_cache_compact(const dsel_cache *cache, const int32_t *page_table, int64_t table_ld,
+                                        int64_t max_pages, const int32_t *seq_len, const int32_t *path,
+                                        const int32_t *n_keep, int64_t batch, int64_t block, int32_t *new_len,
+                                        dsel_stream_t stream) {
+    dsel_status st = check_tree(batch, block);
+    if (st != DSEL_OK) return st;
+    CompactParams p{};
+    if ((st = check_cache(cache, &p.c)) != DSEL_OK) return st;
+    if ((st = check_table(page_table, table_ld, max_pages, cache->page_size, seq_len, batch, block, nullptr, &p.t)) !=
+        DSEL_OK)
+        return st;
+    if (batch == 0) return DSEL_OK;
+    if (!path || !n_keep || !new_len || new_len == seq_len) return DSEL_E_ARG;
+    if (!aligned(path, 4) || !aligned(n_keep, 4) || !aligned(new_len, 4)) return DSEL_E_ALIGN;
+    p.path = path;
+    p.n_keep = n_keep;
+    p.new_len = new_len;
+    p.T = (int)block;
+    const int64_t vecs = 2 * (int64_t)p.c.layers * p.c.heads * p.c.vecs;
+    return launch((const void *)cache_compact_kernel, dim3((unsigned)((vecs + 255) / 256), (unsigned)batch), dim3(256),
+                  &p, 0, stream);
+}
+
+namespace {
+
+dsel_status check_pages(const dsel_pages *g, const int32_t *arg, PoolParams *p) {
+    if (!g) return DSEL_E_ARG;
+    if (g->rows < 0 || g->rows > DSEL_MAX_ROWS || g->max_pages < 1 || g->table_ld < g->max_pages ||
+        g->num_pages < 1 || g->num_pages > INT_MAX - 32768 || g->page_size < 1 || g->page_size > DSEL_MAX_PAGE ||
+        g->max_pages > (INT_MAX - DSEL_MAX_PAGE) / g->page_size || g->table_ld > INT64_MAX / 8 / DSEL_MAX_ROWS)
+        return DSEL_E_ARG;
+    if (g->rows == 0) return DSEL_OK;
+    if (!g->table || !g->row_pages || !g->seq_len || !g->refcount || !arg) return DSEL_E_ARG;
+    if (!aligned(g->table, 4) || !aligned(g->row_pages, 4) || !aligned(g->seq_len, 4) || !aligned(g->refcount, 4) ||
+        !aligned(arg, 4))
+        return DSEL_E_ALIGN;
+    p->table = g->table;
+    p->ld = g->table_ld;
+    p->rows = (int)g->rows;
+    p->max_pages = (int)g->max_pages;
+    p->row_pages = g->row_pages;
+    p->seq_len = g->seq_len;
+    p->refcount = g->refcount;
+    p->num_pages = g->num_pages;
+    p->page_size = (int)g->page_size;
+    p->arg = arg;
+    return DSEL_OK;
+}
+
+}  // namespace
+
+DSEL_API dsel_status dsel_pages_reserve(const dsel_pages *pages, const int32_t *extra, int32_t *granted,
+                                        dsel_stream_t stream) {
+    PoolParams p{};
+    dsel_status st = check_pages(pages, extra, &p);
+    if (st != DSEL_OK || pages->rows == 0) return st;
+    if (!granted) return DSEL_E_ARG;
+    if (!aligned(granted, 4)) return DSEL_E_ALIGN;
+    p.granted = granted;
+    return launch((const void *)pool_give_kernel<false>, dim3(1), dim3(1024), &p, 0, stream);
+}
+
+DSEL_API size_t dsel_pages_fork_workspace_bytes(int64_t rows) {
+    return rows <= 0 || rows > DSEL_MAX_ROWS ? 0 : (size_t)rows * sizeof(int32_t);
+}
+
+DSEL_API dsel_status dsel_pages_fork(const dsel_pages *pages, const int32_t *src, const dsel_cache *cache,
+                                     int32_t *granted, void *workspace, size_t workspace_bytes, dsel_stream_t stream) {
+    PoolParams p{};
+    CacheView c{};
+    dsel_status st = check_pages(pages, src, &p);
+    if (st != DSEL_OK) return st;
+    if ((st = check_cache(cache, &c)) != DSEL_OK) return st;
+    if (cache->num_pages != pages->num_pages || cache->page_size != pages->page_size) return DSEL_E_ARG;
+    if (pages->rows == 0) return DSEL_OK;
+    if (!granted) return DSEL_E_ARG;
+    if (!aligned(granted, 4)) return DSEL_E_ALIGN;
+    if (!workspace || workspace_bytes < dsel_pages_fork_workspace_bytes(pages->rows)) return DSEL_E_WORKSPACE;
+    if (!aligned(workspace, 4)) return DSEL_E_ALIGN;
+    p.granted = granted;
+    p.plan = (int32_t *)workspace;
+    st = launch((const void *)pool_give_kernel<true>, dim3(1), dim3(1024), &p, 0, stream);
+    if (st != DSEL_OK) return st;
+    const int chunks = (c.page_size + kForkSlots - 1) / kForkSlots;
+    void *args[] = {&p, &c};
+    return hipLaunchKernel((const void *)pages_fork_kernel, dim3((unsigned)(1 + 2 * c.layers * chunks), (unsigned)p.rows),
+                           dim3(256), args, 0, (hipStream_t)stream) == hipSuccess ? DSEL_OK : DSEL_E_HIP;
+}
+
+DSEL_API dsel_status dsel_pages_free(const dsel_pages *pages, const int32_t *which, dsel_stream_t stream) {
+    PoolParams p{};
+    dsel_status st = check_pages(pages, which, &p);
+    if (st != DSEL_OK || pages->rows == 0) return st;
+    return launch((const void *)pages_free_kernel, dim3((unsigned)p.rows), dim3(256), &p, 0, stream);
 }
 
 // ---- verify ----------------------------------------------------------------

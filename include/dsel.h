@@ -70,12 +70,18 @@ typedef enum {
     DSEL_E_HIP = -5        /* a HIP runtime call or kernel launch failed */
 } dsel_status;
 
-typedef enum { DSEL_F32 = 0, DSEL_BF16 = 1 } dsel_dtype;
+/* E4M3 (8 bits: 4 of exponent, 3 of mantissa, largest value 448, one NaN per
+ * sign, no infinity) is a type of K/V caches only. */
+typedef enum { DSEL_F32 = 0, DSEL_BF16 = 1, DSEL_E4M3 = 2 } dsel_dtype;
 typedef enum { DSEL_GREEDY = 0, DSEL_SAMPLED = 1 } dsel_walk_mode;
 
 /* Device error word bits (see dsel_device_error). */
 #define DSEL_DEVERR_TOKEN_RANGE 1 /* dsel_project met a token id outside [0, vocab) */
 #define DSEL_DEVERR_BLOCK_LEN 2   /* a block_len entry outside [0, block] */
+#define DSEL_DEVERR_SEQ_LEN 4     /* a row's length or page count that its table row cannot hold */
+#define DSEL_DEVERR_PAGE 8        /* a page id in use outside [0, num_pages), or freed once too often */
+#define DSEL_DEVERR_TREE 16       /* a parent or path entry that is no tree's */
+#define DSEL_DEVERR_POOL 32       /* the pool holds too few free pages */
 
 /* Bytes of device workspace dsel_select_topk needs for `rows` = batch*block rows
  * of `vocab` logits of type `dt` (0 when it needs none).  Returns 0 for
@@ -442,6 +448,213 @@ dsel_status dsel_dyn_conv(const uint16_t *x, const uint16_t *x_prev, const uint1
                           const uint16_t *W_c, int64_t batch, int64_t block,
                           const int32_t *block_len, int64_t d, uint16_t *y, void *workspace,
                           size_t workspace_bytes, dsel_stream_t stream);
+
+/* ---- the cache side of verifying drafted tokens --------------------------------
+ *
+ * Between the walk and dsel_verify the target model runs over the drafted
+ * tokens.  Its attention reads a paged K/V cache under a mask that says which
+ * drafted token sees which; afterwards the kept tokens' rows stay in the cache.
+ * ([P1] Method, last paragraph, and Setup; [P3] "One pass to draft, one pass to
+ * verify".)  The calls below are that side of a step, for a block drafted as a
+ * chain or as a tree.  One step of a batch:
+ *   dsel_pages_reserve       pages for the drafted tokens
+ *   dsel_cache_append        per layer: their K and V behind the cached ones
+ *   dsel_tree_attn           per layer: attention under dsel_tree_mask's bits
+ *   dsel_tree_accept         which nodes the target's own tokens keep
+ *   dsel_cache_compact       the kept nodes' rows moved together, all layers
+ * and, between requests, dsel_pages_fork and dsel_pages_free.
+ *
+ * Trees.  `block` tokens per batch row in the padded layout [batch, block], row
+ * b holding block_len[b] of them (NULL: block).  Node 0 is the last verified
+ * token, whose K and V are not in the cache yet; parent[b, 0] = -1 and
+ * 0 <= parent[b, i] < i.  A chain is the tree parent[b, i] = i - 1.  Another
+ * parent sets DSEL_DEVERR_TREE and makes its node a root of its own, which no
+ * path reaches.  1 <= block <= DSEL_MAX_TREE, 0 <= batch <= DSEL_MAX_TREE_BATCH.
+ *
+ * Caches.  K and V of one or more layers in pages of page_size slots, which all
+ * layers of a row share: position p of batch row b is slot p % page_size of
+ * page page_table[b][p / page_size].  seq_len[b] positions are cached; node i
+ * of row b is at position seq_len[b] + i.  A row whose seq_len is negative, or
+ * whose positions in use pass max_pages * page_size, is treated as an empty
+ * block and sets DSEL_DEVERR_SEQ_LEN.  Entries of page_table past the positions
+ * in use are never read; a page id in use outside [0, num_pages) sets
+ * DSEL_DEVERR_PAGE and its positions are seen by no query (attention), or not
+ * written (append), or leave the whole row as it was (compact). */
+#define DSEL_MAX_TREE 256          /* nodes of a tree */
+#define DSEL_MAX_TREE_BATCH 65535  /* batch rows of these calls */
+#define DSEL_MAX_HEAD_DIM 256
+#define DSEL_MAX_HEADS 1024
+#define DSEL_MAX_LAYERS 1024
+#define DSEL_MAX_PAGE 65536        /* slots of a page */
+#define DSEL_MAX_ROWS 4096         /* rows of a page table under dsel_pages_* */
+
+/* A paged cache.  Element e of head h at a slot of a page of a layer is at
+ * layer * layer_stride + page * page_stride + slot * slot_stride +
+ * head * head_stride + e in both k and v (strides in elements, any order of
+ * them, so tokens-first and heads-first pages, and K and V interleaved, all
+ * fit).  dt is DSEL_BF16, or DSEL_E4M3 with a scale for each layer and head: an
+ * element stands for its 8-bit value times the scale.
+ * Requirements: k, v 16-byte aligned; dim and every stride of an extent above
+ * one a multiple of 16 bytes; those strides >= dim; elements of different
+ * (layer, page, slot, head) distinct; 1 <= dim <= DSEL_MAX_HEAD_DIM,
+ * heads <= DSEL_MAX_HEADS, layers <= DSEL_MAX_LAYERS, page_size <=
+ * DSEL_MAX_PAGE, max_pages * page_size < 2^31 - DSEL_MAX_PAGE. */
+typedef struct {
+    void *k, *v;
+    dsel_dtype dt;
+    int64_t layers, layer_stride;
+    int64_t num_pages, page_stride;
+    int64_t page_size, slot_stride;
+    int64_t heads, head_stride;
+    int64_t dim;
+    const float *k_scale, *v_scale; /* [layers, heads], E4M3 only; NULL = 1 */
+} dsel_cache;
+
+/* tree_mask -- which nodes each node sees, and how deep it lies.
+ *   mask   out [batch, block, ceil(block / 32)] int32: bit j % 32 of word j / 32
+ *          of row i is set for j = i and every node above i.
+ *   depth  out [batch, block] int32 (nullable): 0 at the root, one more per
+ *          level: node i's rotary position is seq_len[b] + depth.
+ * Rows of nodes past block_len[b] are not written. */
+dsel_status dsel_tree_mask(const int32_t *parent, int64_t batch, int64_t block, const int32_t *block_len,
+                           int32_t *mask, int32_t *depth, dsel_stream_t stream);
+
+/* tree_attn -- attention of the drafted tokens over the cache and each other,
+ * for one layer:
+ *   z_ij = scale <q_i, K_j>,  out_i = sum_j softmax_j(z_ij) V_j,  lse_i = ln sum_j e^{z_ij}
+ * over the seq_len[b] cached positions, which every node sees, and the nodes
+ * whose bits are set in its mask row.  Query head h reads K/V head
+ * h / (q_heads / heads).
+ *   q      bf16: element e of head h of node t of row b at b * q_batch +
+ *          t * q_token + h * q_head + e.
+ *   mask   [batch, block, ceil(block / 32)] int32 as dsel_tree_mask writes it,
+ *          or any other visibility between the nodes (a drafter's own block
+ *          that sees all of itself, for one); bits past block_len[b] are
+ *          ignored.  NULL: node i sees nodes 0 .. i (a chain).
+ *   out    [batch, block, q_heads, dim] bf16, rounded once to nearest even.
+ *   lse    [batch, block, q_heads] fp32 (nullable).
+ * A node that sees nothing (no cached position and an empty mask row) gets
+ * out = 0 and lse = -inf.  What a node does not see never affects its result,
+ * infinities and NaN among it.  Rows of nodes past block_len[b] are not
+ * written.
+ * Arithmetic: the products of q and K are exact bf16 products summed in fp32
+ * (E4M3 values are exact in bf16, the scales are applied to the fp32 sums); the
+ * softmax's maximum, weights and sum are fp32; the weights are rounded to bf16
+ * for their products with V, which are summed in fp32.
+ *   workspace  dsel_tree_attn_workspace_bytes() bytes, 16-byte aligned;
+ *              contents need no initialisation.  Calls that overlap need one
+ *              each.
+ * Requirements: cache->layers == 1 and cache->heads divides q_heads; q, out
+ * 16-byte aligned, q's strides multiples of 8; 0 < scale < inf; table_ld >=
+ * max_pages. */
+typedef struct {
+    const uint16_t *q;
+    int64_t q_batch, q_token, q_head;
+    int64_t batch, block, q_heads;
+    const int32_t *block_len;
+    const int32_t *page_table; /* [batch][table_ld] */
+    int64_t table_ld, max_pages;
+    const int32_t *seq_len; /* [batch] */
+    const int32_t *mask;
+    float scale;
+    uint16_t *out;
+    float *lse;
+} dsel_tree_attn_args;
+size_t dsel_tree_attn_workspace_bytes(int64_t batch, int64_t block, int64_t q_heads, int64_t kv_heads, int64_t dim);
+dsel_status dsel_tree_attn(const dsel_tree_attn_args *args, const dsel_cache *cache, void *workspace,
+                           size_t workspace_bytes, dsel_stream_t stream);
+
+/* tree_accept -- the path of the tree that the target keeps (dsel_verify's step
+ * for a tree): from node 0, go to the lowest child whose token is the target's
+ * token after the current node, while there is one.  With the target's arg max
+ * as its token this is greedy verification; with a draw from the target's own
+ * distribution after every node it is lossless sampling, since every kept token
+ * and the last one are then draws of the target.
+ *   parent, tok  [batch, block] int32: the tree and its tokens (tok[b, 0], the
+ *                verified token, is not read).
+ *   target_tok   the target's token after each node, node t of row b at
+ *                (b * block + t) * target_stride (1 for a plain array; DSEL_K
+ *                takes the first of dsel_select_topk's ids, the arg max).
+ *   n_keep   out [batch] int32: nodes kept, the verified one included (0 for
+ *            an empty block): one more than the accepted tokens.
+ *   path     out [batch, block] int32: the kept nodes in order, -1 behind them.
+ *   out_tok  out [batch, block] int32: the accepted tokens and, last, the
+ *            target's token after the last kept node; -1 behind them. */
+dsel_status dsel_tree_accept(const int32_t *parent, const int32_t *tok, const int32_t *target_tok,
+                             int64_t target_stride, int64_t batch, int64_t block, const int32_t *block_len,
+                             int32_t *n_keep, int32_t *path, int32_t *out_tok, dsel_stream_t stream);
+
+/* cache_append -- K and V of new tokens written behind the cached ones, at
+ * positions seq_len[b] + t, t < block_len[b], of every layer.
+ *   k_new, v_new  bf16: element e of head h of token t of row b of layer l at
+ *                 l * strides[0] + b * strides[1] + t * strides[2] + h *
+ *                 strides[3] + e (multiples of 8; the same for K and V).
+ * E4M3 caches take x / scale (one fp32 rounding), held to +-448 and rounded to
+ * nearest even.  seq_len is not changed.  The pages written must be held by
+ * their row alone, as dsel_pages_reserve and dsel_pages_fork leave them.
+ * `block` may be of any length here (a whole prompt). */
+dsel_status dsel_cache_append(const uint16_t *k_new, const uint16_t *v_new, const int64_t strides[4],
+                              const dsel_cache *cache, const int32_t *page_table, int64_t table_ld,
+                              int64_t max_pages, const int32_t *seq_len, int64_t batch, int64_t block,
+                              const int32_t *block_len, dsel_stream_t stream);
+
+/* cache_compact -- keeps a path of the appended nodes: in every layer, the rows
+ * at positions seq_len[b] + path[b, i] move to seq_len[b] + i, i < n_keep[b].
+ *   path     [batch, block] int32, ascending in its first n_keep[b] entries and
+ *            below block; n_keep [batch] int32, 0 <= n_keep[b] <= block.  Other
+ *            values set DSEL_DEVERR_TREE and leave the row as it was.
+ *   new_len  out [batch] int32: seq_len[b] + n_keep[b] (seq_len[b] for a row
+ *            left as it was); must not be seq_len itself. */
+dsel_status dsel_cache_compact(const dsel_cache *cache, const int32_t *page_table, int64_t table_ld,
+                               int64_t max_pages, const int32_t *seq_len, const int32_t *path,
+                               const int32_t *n_keep, int64_t batch, int64_t block, int32_t *new_len,
+                               dsel_stream_t stream);
+
+/* The pool of pages behind a table of rows (all arrays are the caller's, in
+ * device memory, updated in place):
+ *   table      [rows][table_ld] int32: the pages of each row.
+ *   row_pages  [rows] int32: how many entries of its table row a row holds.
+ *   seq_len    [rows] int32: cached positions of each row.
+ *   refcount   [num_pages] int32: rows that hold each page; 0 = free.  A pool
+ *              starts as zeros; a page to keep out of it counts 1.
+ * Rows are batch rows of the calls above.  Calls on one pool must not overlap.
+ * Requirements: rows <= DSEL_MAX_ROWS, table_ld >= max_pages, pointers 4-byte
+ * aligned. */
+typedef struct {
+    int32_t *table;
+    int64_t table_ld, rows, max_pages;
+    int32_t *row_pages, *seq_len, *refcount;
+    int64_t num_pages, page_size;
+} dsel_pages;
+
+/* pages_reserve -- gives every row the pages that it lacks to hold seq_len[r] +
+ * extra[r] positions (extra [rows] int32 >= 0): the lowest free page ids, in
+ * row order.  A row that holds enough gets none.  All rows get theirs, or, when
+ * the pool is short, none does: granted [1] int32 out is 1 or 0, and 0 sets
+ * DSEL_DEVERR_POOL.  A row whose positions pass max_pages * page_size (or with
+ * a negative length) gets none and sets DSEL_DEVERR_SEQ_LEN. */
+dsel_status dsel_pages_reserve(const dsel_pages *pages, const int32_t *extra, int32_t *granted,
+                               dsel_stream_t stream);
+
+/* pages_fork -- row r becomes a copy of row src[r] (src [rows] int32, -1 = row r
+ * takes no part): its seq_len, the whole pages shared (their counts go up), and
+ * the partial last page copied, in every layer, to a page of its own (the slots
+ * in use; the rest stays as it was), so that both rows can grow.  Many rows may
+ * name one source.  Pages past the source's seq_len are not taken along.  Row r
+ * must hold no page and its source must not be a target itself; another entry
+ * is left out and sets DSEL_DEVERR_SEQ_LEN.  All copies get their pages (the
+ * lowest free ids, in row order) or none takes place, as for pages_reserve.
+ *   cache  every layer of the cache; its num_pages and page_size are the pool's.
+ *   workspace  dsel_pages_fork_workspace_bytes() bytes, 4-byte aligned. */
+size_t dsel_pages_fork_workspace_bytes(int64_t rows);
+dsel_status dsel_pages_fork(const dsel_pages *pages, const int32_t *src, const dsel_cache *cache,
+                            int32_t *granted, void *workspace, size_t workspace_bytes, dsel_stream_t stream);
+
+/* pages_free -- rows with which[r] != 0 (which [rows] int32) give back every
+ * page they hold: counts go down by one, the held table entries become -1,
+ * row_pages and seq_len 0.  A page whose count is 0 already, or whose id is out
+ * of range, sets DSEL_DEVERR_PAGE and is left alone. */
+dsel_status dsel_pages_free(const dsel_pages *pages, const int32_t *which, dsel_stream_t stream);
 
 /* ABI version of this header (major * 100 + minor). */
 int32_t dsel_version(void);
