@@ -1235,10 +1235,43 @@ DSEL_API dsel_status dsel_tree_accept(const int32_t *parent, const int32_t *tok,
     return launch((const void *)tree_accept_kernel, dim3((unsigned)batch), dim3(64), &p, 0, stream);
 }
 
+namespace {
+
+// The kernels of one shape: row waves by how many rows (nodes x query heads of
+// a K/V head) there are, padded head dim by the head dim.
+struct AttnKernels {
+    const void *attn, *join;
+    int threads, rows, wgs, part;
+};
+template <class C>
+AttnKernels attn_kernels() {
+    return {(const void *)tree_attn_kernel<C>, (const void *)tree_attn_join_kernel<C>, C::NT, C::ROWS,
+            kAttnCUs * C::WGS, C::PART};
+}
+template <bool E4M3>
+AttnKernels attn_pick(int64_t rows, int64_t dim) {
+    const int rw = rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
+    if (dim <= 64)
+        return rw == 1 ? attn_kernels<AttnCfg<E4M3, 64, 1, 4, 32>>()
+             : rw == 2 ? attn_kernels<AttnCfg<E4M3, 64, 2, 2, E4M3 ? 64 : 32>>() : attn_kernels<AttnCfg<E4M3, 64, 4, 1, 64>>();
+    if (dim <= 128)
+        return rw == 1 ? attn_kernels<AttnCfg<E4M3, 128, 1, 4, 32>>()
+             : rw == 2 ? attn_kernels<AttnCfg<E4M3, 128, 2, 2, E4M3 ? 64 : 32>>() : attn_kernels<AttnCfg<E4M3, 128, 4, 1, 64>>();
+    return rw == 1 ? attn_kernels<AttnCfg<E4M3, 256, 1, 2, 32>>()
+         : rw == 2 ? attn_kernels<AttnCfg<E4M3, 256, 2, 1, 32>>() : attn_kernels<AttnCfg<E4M3, 256, 4, 1, 32>>();
+}
+
+}  // namespace
+
 DSEL_API size_t dsel_tree_attn_workspace_bytes(int64_t batch, int64_t block, int64_t q_heads, int64_t kv_heads,
                                                int64_t dim) {
-    (void)batch, (void)block, (void)q_heads, (void)kv_heads, (void)dim;
-    return 0;
+    if (check_tree(batch, block) != DSEL_OK || batch == 0 || kv_heads < 1 || q_heads < 1 || q_heads > DSEL_MAX_HEADS ||
+        q_heads % kv_heads || dim < 1 || dim > DSEL_MAX_HEAD_DIM)
+        return 0;
+    const int64_t rows = block * (q_heads / kv_heads);
+    const AttnKernels a = attn_pick<false>(rows, dim), b = attn_pick<true>(rows, dim);
+    const size_t na = (size_t)a.wgs * 2 * a.part, nb = (size_t)b.wgs * 2 * b.part;
+    return (na > nb ? na : nb) * sizeof(float);
 }
 
 DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cache *cache, void *workspace,
@@ -1266,8 +1299,10 @@ DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cac
         if (stride[i] % 8) return DSEL_E_ALIGN;
         sq[i] = stride[i];
     }
-    if (workspace_bytes < dsel_tree_attn_workspace_bytes(a->batch, a->block, a->q_heads, cache->heads, cache->dim))
+    if (!workspace || workspace_bytes < dsel_tree_attn_workspace_bytes(a->batch, a->block, a->q_heads, cache->heads,
+                                                                       cache->dim))
         return DSEL_E_WORKSPACE;
+    if (!aligned(workspace, 16)) return DSEL_E_ALIGN;
     p.q = (const char *)a->q;
     p.sqb = sq[0];
     p.sqt = sq[1];
@@ -1283,9 +1318,15 @@ DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cac
     p.group = (int)(a->q_heads / cache->heads);
     p.words = (int)(a->block + 31) / 32;
     p.scale = (float)((double)a->scale * 1.4426950408889634);
-    const void *k = cache->dt == DSEL_E4M3 ? (const void *)tree_attn_simple_kernel<true>
-                                           : (const void *)tree_attn_simple_kernel<false>;
-    return launch(k, dim3((unsigned)p.Hq, (unsigned)p.T, (unsigned)p.B), dim3(64), &p, 0, stream);
+    p.part = (float *)workspace;
+    const int64_t rows = a->block * p.group;
+    const AttnKernels k = cache->dt == DSEL_E4M3 ? attn_pick<true>(rows, cache->dim) : attn_pick<false>(rows, cache->dim);
+    p.wgs = k.wgs;
+    const int64_t tiles = a->batch * cache->heads * ((rows + k.rows - 1) / k.rows);
+    if (tiles > INT_MAX) return DSEL_E_ARG;
+    st = launch(k.attn, dim3((unsigned)k.wgs), dim3((unsigned)k.threads), &p, 0, stream);
+    if (st != DSEL_OK) return st;
+    return launch(k.join, dim3((unsigned)tiles), dim3(256), &p, 0, stream);
 }
 
 DSEL_API dsel_status dsel_cache_append(const uint16_t *k_new, const uint16_t *v_new, const int64_t strides[4],

@@ -5,9 +5,29 @@
 // in one pass over the keys with the running maximum m and sum l of the
 // softmax.  Node i of row b sees the row's s cached positions and the nodes
 // whose bit is set in its mask row (no mask: nodes 0..i).
+//
+// Rows.  The nodes of a batch row times the query heads of one K/V head are the
+// rows of one product (r = node * group + head in group), in row tiles of 32 RW.
+// A workgroup is RW x KW waves: RW waves of 32 rows each share the tiles of one
+// of KW groups of keys, whose sums are joined through LDS at the end.  Few rows
+// take many key groups (each wave then streams K and V of its own, with no
+// barrier), many rows take many row waves (each tile is read once for all).
+//
+// Products.  S^T = K Q^T by 32 x 32 x 16 MFMA, so a lane holds scores of one row
+// (l % 32) and its softmax needs one exchange, with lane l ^ 32, for the maximum
+// only.  Its 16 scores of 32 keys are those of keys 8 (i / 4) + 4 (l / 32) +
+// i % 4; taken eight at a time they are already the operand of O^T = V^T P^T,
+// if V^T's keys are taken in the same order.  V lies in LDS by keys; the
+// transposing LDS reads deliver it by columns.
+//
+// Keys move from the cache into a ring of two LDS stages by 16-byte LDS-DMA
+// loads (global_load_lds_dwordx4), one round ahead; page ids one round before
+// that.  16-byte chunk c of tile row `row` lies at chunk c ^ key(row); the keys
+// spread what one LDS pass reads over all 64 banks.
 #pragma once
 
 #include "cache.h"
+#include "project.h"
 
 namespace dsel {
 
@@ -22,73 +42,573 @@ struct TreeAttnParams {
     const int32_t *len;
     int B, T, Hq, D, group, words;
     float scale;  // times log2(e)
+    int wgs;      // workgroups that share the work
+    float *part;  // partial sums
 };
 
-// The simplest form: one wave per node and head; 64 keys at a time, one per
-// lane for the products with q, then one after the other for the values.
-template <bool E4M3>
-__global__ __launch_bounds__(64) void tree_attn_simple_kernel(TreeAttnParams p) {
-    __shared__ float qs[256], ps[64];
-    __shared__ int64_t at[64];
-    const int lane = threadIdx.x, h = blockIdx.x, t = blockIdx.y, b = blockIdx.z;
-    const int n = block_len_of(p.len, b, p.T);
-    if (t >= n) return;
-    const int s = seq_len_of(p.t, b, n, p.c.page_size);
-    if (s < 0) return;
-    const int hk = h / p.group;
-    const uint16_t *q = (const uint16_t *)p.q + b * p.sqb + t * p.sqt + h * p.sqh;
-    for (int e = lane; e < p.D; e += 64) qs[e] = __uint_as_float((uint32_t)q[e] << 16);
-    const float ks = E4M3 && p.c.k_scale ? p.c.k_scale[hk] : 1.0f, vs = E4M3 && p.c.v_scale ? p.c.v_scale[hk] : 1.0f;
-    float m = -__builtin_inff(), l = 0.0f, o[4] = {0, 0, 0, 0};
-    const int total = s + n;
-    auto value = [&](const char *row, int e) {
-        if constexpr (E4M3) return __builtin_amdgcn_cvt_f32_fp8(((const uint8_t *)row)[e], 0);
-        else return __uint_as_float((uint32_t)((const uint16_t *)row)[e] << 16);
-    };
-    for (int k0 = 0; k0 < total; k0 += 64) {
-        const int k = k0 + lane;
-        bool sees = k < total;
-        if (sees && k >= s) {
-            const int j = k - s;
-            sees = p.mask ? (p.mask[((int64_t)b * p.T + t) * p.words + (j >> 5)] >> (j & 31)) & 1 : j <= t;
-        }
-        const int64_t a = sees ? place_of(p.c, p.t, b, k) : -1;
-        sees = a >= 0;
-        __syncthreads();
-        at[lane] = a;
-        float z = -__builtin_inff();
-        if (sees) {
-            const char *row = p.c.k + 16 * (a + hk * p.c.head_stride);
-            float acc = 0.0f;
-            for (int e = 0; e < p.D; ++e) acc += qs[e] * value(row, e);
-            z = acc * p.scale * ks;
-        }
-        float mx = z;
-        for (int x = 1; x < 64; x <<= 1) mx = fmaxf(mx, shfl_idxf(mx, lane ^ x));
-        const float mn = fmaxf(m, mx), ms = mn == -__builtin_inff() ? 0.0f : mn;
-        const float w = sees ? exp2f(z - ms) : 0.0f, alpha = exp2f(m - ms);
-        ps[lane] = w;
-        float sum = w;
-        for (int x = 1; x < 64; x <<= 1) sum += shfl_idxf(sum, lane ^ x);
-        l = l * alpha + sum;
-        m = mn;
-        __syncthreads();
-        for (int i = 0; i < 4; ++i) o[i] *= alpha;
-        for (int j = 0; j < 64; ++j) {
-            if (at[j] < 0) continue;
-            const char *row = p.c.v + 16 * (at[j] + hk * p.c.head_stride);
-            for (int i = 0; i < 4; ++i)
-                if (i * 64 + lane < p.D) o[i] += ps[j] * value(row, i * 64 + lane);
+__device__ u32x4 g_attn_zero[1];  // what a key that is none reads (never written)
+
+template <bool E4M3_, int DP_, int RW_, int KW_, int KT_>
+struct AttnCfg {
+    static constexpr bool E4M3 = E4M3_;
+    static constexpr int DP = DP_, RW = RW_, KW = KW_, KT = KT_;  // padded head dim, row waves, key groups, keys a tile
+    static constexpr int RB = DP * (E4M3 ? 1 : 2), CH = RB / 16;  // bytes and 16-byte chunks of a tile row
+    static constexpr int NT = 64 * RW * KW, ROWS = 32 * RW, ROUND = KT * KW;
+    static constexpr int TILE = KT * RB, LDS = KW * 4 * TILE;  // K and V, two stages
+    static constexpr int LOADS = TILE / 1024 / RW;             // LDS-DMA loads of a wave per K or V tile
+    static constexpr int PART = ROWS * (DP + 2);               // floats of one partial result
+    // workgroups on a CU, as far as LDS allows (160 KB) and 512 registers a lane:
+    // heads of 256 need more than 256 of them
+    static constexpr int WGS = DP > 128 ? (NT == 128 && LDS <= 80 * 1024 ? 2 : 1) : LDS <= 80 * 1024 ? 2 : 1;
+    static constexpr int WAVES = WGS * NT / 256 < 1 ? 1 : WGS * NT / 256;  // per SIMD
+    static_assert(LOADS * 1024 * RW == TILE && KT <= 64 && KT % 32 == 0 && DP % 32 == 0, "tile geometry");
+
+    __device__ static __forceinline__ int kkey(int row) {
+        return RB >= 256 ? row & 15 : RB == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+    }
+    // rows that one transposing read takes together: 4 (16 bits) or 4 + 4 eight apart (8 bits)
+    __device__ static __forceinline__ int vkey(int row) {
+        if constexpr (!E4M3) return RB >= 256 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
+        else if constexpr (RB >= 256) return ((row & 3) | ((row >> 1) & 4)) << 1;
+        else if constexpr (RB == 128) return (((row >> 1) & 1) | ((row >> 2) & 2)) << 1;
+        else return ((row >> 3) & 1) << 1;
+    }
+};
+
+// The work: units of one round (ROUND keys of one row tile), row by row of the
+// batch, within it K/V head by head, row tile by row tile, round by round;
+// workgroup w takes units [w U / W, (w + 1) U / W).  So every workgroup has the
+// same number of rounds whatever the lengths, and a tile's rounds are split
+// over as many workgroups as it takes; the partial sums of a split tile are
+// joined by tree_attn_join_kernel.
+struct AttnRow {
+    int s, n;        // cached positions, nodes (0: nothing to do)
+    int rts, rounds; // row tiles, rounds of each
+};
+template <class C>
+__device__ __forceinline__ AttnRow attn_row(const TreeAttnParams &p, int64_t b) {
+    AttnRow r;
+    r.n = block_len_of(p.len, b, p.T);
+    r.s = r.n > 0 ? seq_len_of(p.t, b, r.n, p.c.page_size) : 0;
+    if (r.s < 0) r.n = r.s = 0;
+    r.rts = (r.n * p.group + C::ROWS - 1) / C::ROWS;
+    r.rounds = (int)(((int64_t)r.s + r.n + C::ROUND - 1) / C::ROUND);
+    return r;
+}
+template <class C>
+__device__ __forceinline__ int64_t attn_units(const TreeAttnParams &p, int64_t b) {
+    const AttnRow r = attn_row<C>(p, b);
+    return (int64_t)r.rts * p.c.heads * r.rounds;
+}
+
+__device__ __forceinline__ int64_t wave_incl_scan64(int64_t x) {
+    const uint32_t lane = lane_id();
+#pragma unroll
+    for (uint32_t o = 1; o < 64; o <<= 1) {
+        const int64_t y = (int64_t)shfl_idx64((uint64_t)x, lane >= o ? lane - o : lane);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+// How many workgroups share U units: all, but none gets less than kAttnMinUnits rounds
+constexpr int kAttnCUs = 256;
+constexpr int kAttnMinUnits = 1;
+__device__ __forceinline__ int64_t attn_shares(const TreeAttnParams &p, int64_t U) {
+    const int64_t most = (U + kAttnMinUnits - 1) / kAttnMinUnits;
+    return most < p.wgs ? most : p.wgs;
+}
+
+// The units of all rows (returned), and the row that unit u lies in with the
+// units before it.  A whole wave calls it; lane k first sums the rows of its
+// own range of ceil(B / 64).
+template <class C>
+__device__ __forceinline__ int64_t attn_total(const TreeAttnParams &p, int64_t *mine) {
+    const int64_t c = ((int64_t)p.B + 63) / 64, b0 = lane_id() * c;
+    int64_t sum = 0;
+    for (int64_t k = 0; k < c; ++k)
+        if (b0 + k < p.B) sum += attn_units<C>(p, b0 + k);
+    const int64_t incl = wave_incl_scan64(sum);
+    *mine = incl;
+    return (int64_t)readlane64((uint64_t)incl, 63);
+}
+template <class C>
+__device__ __forceinline__ int attn_find(const TreeAttnParams &p, int64_t incl, int64_t u, int64_t *before) {
+    const int64_t c = ((int64_t)p.B + 63) / 64;
+    const int j = __builtin_ctzll(ballot(incl > u));  // u < the total, so some lane's sum passes it
+    int64_t at = j ? (int64_t)readlane64((uint64_t)incl, j - 1) : 0;
+    int64_t b = j * c;
+    if (c > 1) {
+        for (;;) {
+            const int64_t x = attn_units<C>(p, b);
+            if (at + x > u) break;
+            at += x;
+            ++b;
         }
     }
-    const int64_t r = ((int64_t)b * p.T + t) * p.Hq + h;
-    const float inv = l > 0.0f || l != l ? vs / l : 0.0f;
-    for (int i = 0; i < 4; ++i)
-        if (i * 64 + lane < p.D) {
-            const __bf16 x = (__bf16)(o[i] * inv);
-            p.out[r * p.D + i * 64 + lane] = __builtin_bit_cast(uint16_t, x);
+    *before = at;
+    return (int)b;
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ bf16x8 widen_e4m3(uint32_t a, uint32_t b) {
+    const bf16x2 w0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, 1.0f, false);
+    const bf16x2 w1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, 1.0f, true);
+    const bf16x2 w2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)b, 1.0f, false);
+    const bf16x2 w3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)b, 1.0f, true);
+    return bf16x8{w0[0], w0[1], w1[0], w1[1], w2[0], w2[1], w3[0], w3[1]};
+}
+
+#define DSEL_LDS __attribute__((address_space(3)))
+
+// 8 keys (16 kk + 8 (e / 4) + 4 (l / 32) + e % 4 of the 32 from tile row `sub`
+// on) of V's column 32 mb + l % 32
+template <class C>
+__device__ __forceinline__ bf16x8 v_operand(const char *vt, int sub, int kk, int mb) {
+    const int l = lane_id(), h = l >> 5;
+    if constexpr (!C::E4M3) {
+        const int row = sub + 16 * kk + 4 * h + ((l & 15) >> 2);
+        const int chunk = 4 * mb + 2 * ((l >> 4) & 1) + ((l & 3) >> 1);
+        const char *a = vt + row * C::RB + ((chunk ^ C::vkey(row)) << 4) + ((l & 1) << 3);
+        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DSEL_LDS s16x4 *)a);
+        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DSEL_LDS s16x4 *)(a + 8 * C::RB));
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+        const int k = (l & 15) >> 1, row = sub + 16 * kk + 8 * (k >> 2) + 4 * h + (k & 3);
+        const int chunk = 2 * mb + ((l >> 4) & 1);
+        const char *a = vt + row * C::RB + ((chunk ^ C::vkey(row)) << 4) + ((l & 1) << 3);
+        const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((DSEL_LDS i32x2 *)a);
+        return widen_e4m3((uint32_t)x[0], (uint32_t)x[1]);
+    }
+}
+
+// Infinities and NaN among the values of a tile.  0 times those is no 0, so a
+// row that does not see their key would catch them.  A tile in which some rows
+// do not see every key is looked through for them; if it holds any they are
+// taken out of the products and counted apart, among the keys that each row
+// sees: +inf as 1, -inf as 32, NaN as 1024 (below 32 of each per product, so
+// the sum tells them apart).
+template <class C>
+__device__ __forceinline__ bool tile_special(const char *vt) {
+    bool r = false;
+#pragma unroll 1
+    for (int i = lane_id() * 16; i < C::TILE; i += 1024) {
+        const u32x4 w = *(const u32x4 *)(vt + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if constexpr (C::E4M3) r |= (((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+            else r |= (w[k] & 0x7F800000u) == 0x7F800000u || (w[k] & 0x7F80u) == 0x7F80u;
+    }
+    return ballot(r) != 0;
+}
+__device__ __forceinline__ bf16x8 only_finite(const bf16x8 &v) {
+    u32x4 w = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu;
+        if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
+    }
+    return __builtin_bit_cast(bf16x8, w);
+}
+__device__ __forceinline__ bf16x8 special_codes(const bf16x8 &v) {
+    u32x4 w = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t c = 0;
+#pragma unroll
+        for (int k = 0; k < 32; k += 16) {
+            const uint32_t x = (w[i] >> k) & 0xFFFFu;
+            if ((x & 0x7F80u) == 0x7F80u) c |= (x == 0x7F80u ? 0x3F80u : x == 0xFF80u ? 0x4200u : 0x4480u) << k;
         }
-    if (p.lse && lane == 0) p.lse[r] = l > 0.0f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -__builtin_inff();
+        w[i] = c;
+    }
+    return __builtin_bit_cast(bf16x8, w);
+}
+// Adds what the specials of a tile do to column block mb.
+template <class C>
+__device__ __forceinline__ void add_special(floatx16 &o, const char *vt, int mb, uint64_t see) {
+    const int h = lane_id() >> 5;
+#pragma unroll 1
+    for (int step = 0; step < C::KT / 16; ++step) {
+        const uint32_t bits = (uint32_t)(see >> (16 * step + 4 * h));
+        u32x4 seen;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            const int k = 8 * (e >> 2) + (e & 3);
+            seen[e >> 1] = ((bits >> k) & 1 ? 0x3F80u : 0u) | ((bits >> (k + 1)) & 1 ? 0x3F800000u : 0u);
+        }
+        const bf16x8 code = special_codes(v_operand<C>(vt, 32 * (step >> 1), step & 1, mb));
+        const floatx16 n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(code, __builtin_bit_cast(bf16x8, seen), floatx16{}, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int k = (int)n[i];
+            const bool nan = k >= 1024 || ((k & 31) && k >= 32);
+            if (k) o[i] += nan ? __builtin_nanf("") : k >= 32 ? -__builtin_inff() : __builtin_inff();
+        }
+    }
+}
+
+template <class C>
+struct AttnState {
+    floatx16 o[C::DP / 32];
+    float m, l;  // per lane: row l % 32; l: the sum over the lane's own keys
+};
+
+// One tile of KT keys for a wave's 32 rows.  `masked` (one value per wave): bit
+// j of `see` (the lane's row) says whether key j is seen; else all are.
+template <class C>
+__device__ __forceinline__ void attn_tile(AttnState<C> &a, const bf16x8 (&q)[C::DP / 16], const char *kt,
+                                          const char *vt, float c, bool masked, uint64_t see) {
+    const int l = lane_id(), h = l >> 5, r = l & 31;
+    constexpr int NS = C::KT / 32;
+    floatx16 s[NS];
+#pragma unroll
+    for (int sub = 0; sub < NS; ++sub) {
+        s[sub] = floatx16{};
+        const char *row = kt + (sub * 32 + r) * C::RB;
+        const int key = C::kkey(r);
+        if constexpr (!C::E4M3) {
+#pragma unroll
+            for (int ks = 0; ks < C::DP / 16; ++ks) {
+                const bf16x8 x = *(const bf16x8 *)(row + (((2 * ks + h) ^ key) << 4));
+                s[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[ks], s[sub], 0, 0, 0);
+            }
+        } else {
+            // a 16-byte chunk is 16 values: two steps of the product
+#pragma unroll
+            for (int ks = 0; ks < C::DP / 32; ++ks) {
+                const u32x4 x = *(const u32x4 *)(row + (((2 * ks + h) ^ key) << 4));
+                s[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_e4m3(x[0], x[1]), q[2 * ks], s[sub], 0, 0, 0);
+                s[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_e4m3(x[2], x[3]), q[2 * ks + 1], s[sub], 0, 0, 0);
+            }
+        }
+    }
+    bool special = false;
+    if (masked) {
+#pragma unroll
+        for (int sub = 0; sub < NS; ++sub) {
+            const uint32_t w = (uint32_t)(see >> (32 * sub)) >> (4 * h);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (!((w >> (8 * (i >> 2) + (i & 3))) & 1)) s[sub][i] = -__builtin_inff();
+        }
+        special = tile_special<C>(vt);
+    }
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int sub = 0; sub < NS; ++sub)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[sub][i]);
+    top = fmaxf(top, __uint_as_float(xor_lane32<32>(__float_as_uint(top)))) * c;
+    // The running maximum only moves (and the sums are only scaled) when a row's
+    // scores pass it by more than 8: weights stay below 2^8, exact as any others.
+    if (ballot(top > a.m + 8.0f)) {
+        const float m = fmaxf(a.m, top);
+        const float f = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(a.m - m);
+#pragma unroll
+        for (int mb = 0; mb < C::DP / 32; ++mb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) a.o[mb][i] *= f;
+        a.l *= f;
+        a.m = m;
+    }
+    const float ms = a.m == -__builtin_inff() ? 0.0f : a.m;
+#pragma unroll
+    for (int sub = 0; sub < NS; ++sub) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[sub][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[sub][i], c, -ms));
+            sum += s[sub][i];
+        }
+        a.l += sum;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            bf16x8 w;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = (__bf16)s[sub][8 * kk + e];
+#pragma unroll
+            for (int mb = 0; mb < C::DP / 32; ++mb) {
+                bf16x8 v = v_operand<C>(vt, 32 * sub, kk, mb);
+                if (special) v = only_finite(v);
+                a.o[mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w, a.o[mb], 0, 0, 0);
+            }
+        }
+    }
+    if (special) {
+#pragma unroll
+        for (int mb = 0; mb < C::DP / 32; ++mb) add_special<C>(a.o[mb], vt, mb, see);
+    }
+}
+
+// Which of the 32 keys from position `kb` on node t of row b sees, by its mask
+__device__ __forceinline__ uint32_t sees_of(const TreeAttnParams &p, int64_t b, int t, int s, int kb) {
+    const int first = kb - s;  // the node at the first of them
+    if (first <= -32) return ~0u;
+    if (p.mask == nullptr) {
+        const int count = t + 1 - first;
+        return count >= 32 ? ~0u : count <= 0 ? 0u : (1u << count) - 1;
+    }
+    const int32_t *w = p.mask + ((int64_t)b * p.T + t) * p.words;
+    if (first < 0) return ((uint32_t)w[0] << -first) | ((1u << -first) - 1);
+    const int i = first >> 5, sh = first & 31;
+    uint32_t x = i < p.words ? (uint32_t)w[i] >> sh : 0u;
+    if (sh && i + 1 < p.words) x |= (uint32_t)w[i + 1] << (32 - sh);
+    return x;
+}
+
+template <class C>
+__global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnParams p) {
+    __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rw = wave % C::RW, grp = wave / C::RW, h = lane >> 5;
+    int64_t incl;
+    const int64_t U = attn_total<C>(p, &incl);
+    if (U == 0) return;
+    // neighbouring shares on one XCD (workgroup i runs on XCD i % 8): row tiles
+    // that read the same keys then find them in its L2
+    const int64_t W = attn_shares(p, U), per = (W + 7) >> 3;
+    if ((blockIdx.x >> 3) >= per) return;
+    const int64_t share = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if (share >= W) return;
+    int64_t u = share * U / W;
+    const int64_t uend = (share + 1) * U / W;
+    if (u >= uend) return;
+    int64_t before;
+    int b = attn_find<C>(p, incl, u, &before);
+    AttnRow row = attn_row<C>(p, b);
+
+    char *const ring = lds + grp * 4 * C::TILE;
+    while (u < uend) {
+        while (u - before >= (int64_t)row.rts * p.c.heads * row.rounds) {  // on to the next row with work
+            before += (int64_t)row.rts * p.c.heads * row.rounds;
+            row = attn_row<C>(p, ++b);
+        }
+        const int item = (int)((u - before) / row.rounds);
+        const int r0 = (int)((u - before) - (int64_t)item * row.rounds);
+        const int r1 = (int)((int64_t)row.rounds - r0 < uend - u ? row.rounds : r0 + (uend - u));
+        const int hk = item / row.rts, rt = item - hk * row.rts;
+        const int total = row.s + row.n;
+        const char *const kbase = p.c.k + 16 * (hk * p.c.head_stride);
+        const char *const vbase = p.c.v + 16 * (hk * p.c.head_stride);
+        float c = p.scale;
+        bool flip = false;  // a negative scale changes q's sign, so that c stays positive
+        if (C::E4M3 && p.c.k_scale) {
+            const float ks = p.c.k_scale[hk];
+            flip = ks < 0.0f;
+            c = fmaxf(p.scale * fabsf(ks), 1e-37f);
+        }
+
+        // the keys of a round: lane j of every wave looks up key j of its group's tile
+        auto key_pos = [&](int round) { return round * C::ROUND + grp * C::KT + (lane & (C::KT - 1)); };
+        auto page_of = [&](int round) -> int {
+            const int k = key_pos(round);
+            return round < r1 && k < total ? p.t.table[b * p.t.ld + (uint32_t)k / (uint32_t)p.c.page_size] : -1;
+        };
+        auto offset_of = [&](int round, int page) -> int64_t {
+            const int k = key_pos(round);
+            if (k >= total) return -1;
+            if (page < 0 || page >= p.c.num_pages) {
+                device_error(kErrPage);
+                return -1;
+            }
+            return (int64_t)page * p.c.page_stride + (int64_t)((uint32_t)k % (uint32_t)p.c.page_size) * p.c.slot_stride;
+        };
+        auto stage = [&](char *to, int64_t off) {
+#pragma unroll
+            for (int j = 0; j < C::LOADS; ++j) {
+                const int at = (rw * C::LOADS + j) * 1024, byte = at + lane * 16;
+                const int rr = byte / C::RB, ch = (byte % C::RB) / 16;
+                const int64_t o = (int64_t)shfl_idx64((uint64_t)off, rr);
+                const int kc = ch ^ C::kkey(rr), vc = ch ^ C::vkey(rr);
+                const char *ks = o >= 0 && kc < p.c.vecs ? kbase + 16 * (o + kc) : (const char *)g_attn_zero;
+                const char *vs = o >= 0 && vc < p.c.vecs ? vbase + 16 * (o + vc) : (const char *)g_attn_zero;
+                lds_dma16(ks, (uint16_t *)(to + at));
+                lds_dma16(vs, (uint16_t *)(to + C::TILE + at));
+            }
+        };
+        int64_t off = offset_of(r0, page_of(r0));
+        uint64_t ok = ballot(off >= 0);
+        stage(ring, off);
+        int page = page_of(r0 + 1);
+
+        // the lane's row, and its q: eight values of every 16-deep step
+        const int r = rt * C::ROWS + rw * 32 + (lane & 31);
+        const bool live = r < row.n * p.group;
+        const int t = live ? r / p.group : 0, g = live ? r - t * p.group : 0;
+        const uint16_t *qr = (const uint16_t *)p.q + b * p.sqb + t * p.sqt + (hk * p.group + g) * p.sqh;
+        bf16x8 q[C::DP / 16];
+#pragma unroll
+        for (int ks = 0; ks < C::DP / 16; ++ks) {
+            const int d = C::E4M3 ? 32 * (ks >> 1) + 16 * h + 8 * (ks & 1) : 16 * ks + 8 * h;
+            u32x4 w = live && d < p.D ? *(const u32x4 *)(qr + d) : u32x4{0, 0, 0, 0};
+            if (C::E4M3 && flip) w ^= 0x80008000u;
+            q[ks] = __builtin_bit_cast(bf16x8, w);
+        }
+        AttnState<C> a;
+#pragma unroll
+        for (int mb = 0; mb < C::DP / 32; ++mb) a.o[mb] = floatx16{};
+        a.m = -__builtin_inff();
+        a.l = 0.0f;
+
+        for (int round = r0; round < r1; ++round) {
+            const char *cur = ring + ((round - r0) & 1) * 2 * C::TILE;
+            // this round's keys have landed, and nobody still reads the other stage
+            wait_vmcnt_lgkm0<0>();
+            if constexpr (C::RW > 1) wg_barrier();
+            else asm volatile("" ::: "memory");
+            const uint64_t now = ok;
+            if (round + 1 < r1) {
+                off = offset_of(round + 1, page);
+                ok = ballot(off >= 0);
+                stage(ring + ((round + 1 - r0) & 1) * 2 * C::TILE, off);
+                page = page_of(round + 2);
+            }
+            const int kb = round * C::ROUND + grp * C::KT;
+            constexpr uint64_t kAll = ~0ull >> (64 - C::KT);
+            const bool whole = kb + C::KT <= row.s && (now & kAll) == kAll;
+            uint64_t see = now;
+            if (!whole) {
+                if ((now & kAll) == 0) continue;
+                see &= sees_of(p, b, t, row.s, kb) | (C::KT == 64 ? (uint64_t)sees_of(p, b, t, row.s, kb + 32) << 32 : 0);
+            }
+            attn_tile<C>(a, q, cur, cur + C::TILE, c, !whole, see);
+        }
+
+        a.l += __uint_as_float(xor_lane32<32>(__float_as_uint(a.l)));
+        if constexpr (C::KW > 1) {
+            // groups 1.. hand their sums to group 0, register by register
+            constexpr int N = C::DP / 2 + 2;  // floats per lane
+            static_assert((C::KW - 1) * C::RW * N * 256 <= C::LDS, "sums fit the ring");
+            float *mine = (float *)lds + ((grp - 1) * C::RW + rw) * N * 64 + lane;
+            __syncthreads();
+            if (grp > 0) {
+#pragma unroll
+                for (int mb = 0; mb < C::DP / 32; ++mb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) mine[(mb * 16 + i) * 64] = a.o[mb][i];
+                mine[(N - 2) * 64] = a.m;
+                mine[(N - 1) * 64] = a.l;
+            }
+            __syncthreads();
+            if (grp == 0) {
+#pragma unroll 1
+                for (int k = 0; k < C::KW - 1; ++k) {
+                    const float *from = (const float *)lds + (k * C::RW + rw) * N * 64 + lane;
+                    const float fm = from[(N - 2) * 64], fl = from[(N - 1) * 64];
+                    const float m = fmaxf(a.m, fm), ms = m == -__builtin_inff() ? 0.0f : m;
+                    const float fa = __builtin_amdgcn_exp2f(a.m - ms), fb = __builtin_amdgcn_exp2f(fm - ms);
+                    a.l = a.l * fa + fl * fb;
+                    a.m = m;
+#pragma unroll
+                    for (int mb = 0; mb < C::DP / 32; ++mb)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) a.o[mb][i] = a.o[mb][i] * fa + from[(mb * 16 + i) * 64] * fb;
+                }
+            }
+        }
+        if (grp == 0) {
+            if (r0 == 0 && r1 == row.rounds) {
+                const bool some = !(a.l <= 0.0f);  // NaN counts as something
+                const float f = some ? (C::E4M3 && p.c.v_scale ? p.c.v_scale[hk] : 1.0f) / a.l : 0.0f;
+                if (live) {
+                    const int64_t o = (((int64_t)b * p.T + t) * p.Hq + hk * p.group + g);
+#pragma unroll
+                    for (int mb = 0; mb < C::DP / 32; ++mb)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int d = 32 * mb + 8 * i + 4 * h;
+                            if (d >= p.D) continue;
+                            bf16x2 y[2];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) y[e >> 1][e & 1] = (__bf16)(some ? a.o[mb][4 * i + e] * f : 0.0f);
+                            *(uint2 *)(p.out + o * p.D + d) = __builtin_bit_cast(uint2, y);
+                        }
+                    if (p.lse && h == 0)
+                        p.lse[o] = some ? (a.m + __builtin_amdgcn_logf(a.l)) * 0.69314718055994531f : -__builtin_inff();
+                }
+            } else {
+                float *to = p.part + (share * 2 + (r0 == 0)) * C::PART;
+                const int rr = rw * 32 + (lane & 31);
+                if (h == 0) {
+                    to[rr] = a.m;
+                    to[C::ROWS + rr] = a.l;
+                }
+#pragma unroll
+                for (int mb = 0; mb < C::DP / 32; ++mb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const floatx4 y = {a.o[mb][4 * i], a.o[mb][4 * i + 1], a.o[mb][4 * i + 2], a.o[mb][4 * i + 3]};
+                        *(floatx4 *)(to + 2 * C::ROWS + rr * C::DP + 32 * mb + 8 * i + 4 * h) = y;
+                    }
+            }
+        }
+        u += r1 - r0;
+        if (u < uend) {
+            // the ring (and the sums in it) are read no more
+            wait_vmcnt_lgkm0<0>();
+            __syncthreads();
+        }
+    }
+}
+
+// Joins the partial sums of every row tile that several workgroups shared: one
+// workgroup per row tile, DP / 4 threads per row.
+template <class C>
+__global__ __launch_bounds__(256) void tree_attn_join_kernel(TreeAttnParams p) {
+    const int rts_most = (p.T * p.group + C::ROWS - 1) / C::ROWS;
+    const int64_t per = (int64_t)p.c.heads * rts_most;
+    const int b = (int)(blockIdx.x / per), item_most = (int)(blockIdx.x - b * per);
+    const AttnRow row = attn_row<C>(p, b);
+    const int hk = item_most / rts_most, rt = item_most - hk * rts_most;
+    if (rt >= row.rts) return;
+    int64_t incl, first = 0;
+    const int64_t U = attn_total<C>(p, &incl), W = attn_shares(p, U);
+    {
+        const int64_t c = ((int64_t)p.B + 63) / 64;
+        const int j = (int)(b / c);
+        if (j) first = (int64_t)readlane64((uint64_t)incl, j - 1);
+        for (int64_t k = j * c; k < b; ++k) first += attn_units<C>(p, k);
+    }
+    first += (int64_t)(hk * row.rts + rt) * row.rounds;
+    const int64_t last = first + row.rounds - 1;
+    const int64_t w0 = ((first + 1) * W - 1) / U, w1 = ((last + 1) * W - 1) / U;
+    if (w0 == w1) return;
+    // the first share begins the tile (slot 1) unless it also began before it
+    auto part_of = [&](int64_t w) { return p.part + (w * 2 + (w == w0)) * C::PART; };
+    constexpr int TR = C::DP / 4, NR = 256 / TR;
+    const int d = (threadIdx.x % TR) * 4;
+    const int rows = min(C::ROWS, row.n * p.group - rt * C::ROWS);
+    for (int rr = threadIdx.x / TR; rr < rows; rr += NR) {
+        float m = -__builtin_inff();
+        for (int64_t w = w0; w <= w1; ++w) m = fmaxf(m, part_of(w)[rr]);
+        const float ms = m == -__builtin_inff() ? 0.0f : m;
+        float l = 0.0f;
+        floatx4 o = {0, 0, 0, 0};
+        for (int64_t w = w0; w <= w1; ++w) {
+            const float *x = part_of(w);
+            const float f = __builtin_amdgcn_exp2f(x[rr] - ms);
+            l += x[C::ROWS + rr] * f;
+            o += *(const floatx4 *)(x + 2 * C::ROWS + rr * C::DP + d) * f;
+        }
+        const int r = rt * C::ROWS + rr, t = r / p.group, g = r - t * p.group;
+        const int64_t at = ((int64_t)b * p.T + t) * p.Hq + hk * p.group + g;
+        const bool some = !(l <= 0.0f);
+        const float f = some ? (C::E4M3 && p.c.v_scale ? p.c.v_scale[hk] : 1.0f) / l : 0.0f;
+        if (d < p.D) {
+            bf16x2 y[2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e >> 1][e & 1] = (__bf16)(some ? o[e] * f : 0.0f);
+            *(uint2 *)(p.out + at * p.D + d) = __builtin_bit_cast(uint2, y);
+        }
+        if (p.lse && d == 0)
+            p.lse[at] = some ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f : -__builtin_inff();
+    }
 }
 
 }  // namespace dsel
