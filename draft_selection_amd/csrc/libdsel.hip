@@ -1241,12 +1241,12 @@ namespace {
 // a K/V head) there are, padded head dim by the head dim.
 struct AttnKernels {
     const void *attn, *join;
-    int threads, rows, wgs, part;
+    int threads, rows, wgs, part, join_y;
 };
 template <class C>
 AttnKernels attn_kernels() {
     return {(const void *)tree_attn_kernel<C>, (const void *)tree_attn_join_kernel<C>, C::NT, C::ROWS,
-            kAttnCUs * C::WGS, C::PART};
+            kAttnCUs * C::WGS, C::PART, C::ROWS * C::DP / 1024};
 }
 template <bool E4M3>
 AttnKernels attn_pick(int64_t rows, int64_t dim) {
@@ -1270,7 +1270,7 @@ DSEL_API size_t dsel_tree_attn_workspace_bytes(int64_t batch, int64_t block, int
         return 0;
     const int64_t rows = block * (q_heads / kv_heads);
     const AttnKernels a = attn_pick<false>(rows, dim), b = attn_pick<true>(rows, dim);
-    const size_t na = (size_t)a.wgs * 2 * a.part, nb = (size_t)b.wgs * 2 * b.part;
+    const size_t na = (size_t)a.wgs * (2 * a.part + kJoinWords), nb = (size_t)b.wgs * (2 * b.part + kJoinWords);
     return (na > nb ? na : nb) * sizeof(float);
 }
 
@@ -1322,11 +1322,10 @@ DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cac
     const int64_t rows = a->block * p.group;
     const AttnKernels k = cache->dt == DSEL_E4M3 ? attn_pick<true>(rows, cache->dim) : attn_pick<false>(rows, cache->dim);
     p.wgs = k.wgs;
-    const int64_t tiles = a->batch * cache->heads * ((rows + k.rows - 1) / k.rows);
-    if (tiles > INT_MAX) return DSEL_E_ARG;
+    p.join = (int32_t *)(p.part + (int64_t)k.wgs * 2 * k.part);
     st = launch(k.attn, dim3((unsigned)k.wgs), dim3((unsigned)k.threads), &p, 0, stream);
     if (st != DSEL_OK) return st;
-    return launch(k.join, dim3((unsigned)tiles), dim3(256), &p, 0, stream);
+    return launch(k.join, dim3((unsigned)k.wgs, (unsigned)k.join_y), dim3(256), &p, 0, stream);
 }
 
 DSEL_API dsel_status dsel_cache_append(const uint16_t *k_new, const uint16_t *v_new, const int64_t strides[4],

@@ -44,7 +44,9 @@ struct TreeAttnParams {
     float scale;  // times log2(e)
     int wgs;      // workgroups that share the work
     float *part;  // partial sums
+    int32_t *join;  // [wgs][kJoinWords]: the row tile that begins in a workgroup's share and ends in a later one's
 };
+constexpr int kJoinWords = 8;
 
 __device__ u32x4 g_attn_zero[1];  // what a key that is none reads (never written)
 
@@ -367,6 +369,8 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rw = wave % C::RW, grp = wave / C::RW, h = lane >> 5;
+    int32_t *const join = p.join + blockIdx.x * kJoinWords;
+    if (threadIdx.x == 0) join[0] = -1;
     int64_t incl;
     const int64_t U = attn_total<C>(p, &incl);
     if (U == 0) return;
@@ -512,6 +516,15 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
                 }
             }
         }
+        if (threadIdx.x == 0 && r0 == 0 && r1 < row.rounds) {
+            // the tile goes on in the shares up to that of its last round
+            join[0] = b;
+            join[1] = hk;
+            join[2] = rt;
+            join[3] = (int)share;
+            join[4] = (int)((((u - r0) + row.rounds) * W - 1) / U);
+            join[5] = row.n;
+        }
         if (grp == 0) {
             if (r0 == 0 && r1 == row.rounds) {
                 const bool some = !(a.l <= 0.0f);  // NaN counts as something
@@ -557,58 +570,61 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
     }
 }
 
-// Joins the partial sums of every row tile that several workgroups shared: one
-// workgroup per row tile, DP / 4 threads per row.
+// Joins the partial sums of the row tiles that several workgroups shared:
+// workgroup (i, y) takes 1024 / DP rows of the tile that workgroup i of the
+// attention began and did not end; a thread takes four columns of a row and has
+// the parts of eight shares in flight at a time.
 template <class C>
 __global__ __launch_bounds__(256) void tree_attn_join_kernel(TreeAttnParams p) {
-    const int rts_most = (p.T * p.group + C::ROWS - 1) / C::ROWS;
-    const int64_t per = (int64_t)p.c.heads * rts_most;
-    const int b = (int)(blockIdx.x / per), item_most = (int)(blockIdx.x - b * per);
-    const AttnRow row = attn_row<C>(p, b);
-    const int hk = item_most / rts_most, rt = item_most - hk * rts_most;
-    if (rt >= row.rts) return;
-    int64_t incl, first = 0;
-    const int64_t U = attn_total<C>(p, &incl), W = attn_shares(p, U);
-    {
-        const int64_t c = ((int64_t)p.B + 63) / 64;
-        const int j = (int)(b / c);
-        if (j) first = (int64_t)readlane64((uint64_t)incl, j - 1);
-        for (int64_t k = j * c; k < b; ++k) first += attn_units<C>(p, k);
-    }
-    first += (int64_t)(hk * row.rts + rt) * row.rounds;
-    const int64_t last = first + row.rounds - 1;
-    const int64_t w0 = ((first + 1) * W - 1) / U, w1 = ((last + 1) * W - 1) / U;
-    if (w0 == w1) return;
-    // the first share begins the tile (slot 1) unless it also began before it
-    auto part_of = [&](int64_t w) { return p.part + (w * 2 + (w == w0)) * C::PART; };
-    constexpr int TR = C::DP / 4, NR = 256 / TR;
-    const int d = (threadIdx.x % TR) * 4;
-    const int rows = min(C::ROWS, row.n * p.group - rt * C::ROWS);
-    for (int rr = threadIdx.x / TR; rr < rows; rr += NR) {
-        float m = -__builtin_inff();
-        for (int64_t w = w0; w <= w1; ++w) m = fmaxf(m, part_of(w)[rr]);
-        const float ms = m == -__builtin_inff() ? 0.0f : m;
-        float l = 0.0f;
-        floatx4 o = {0, 0, 0, 0};
-        for (int64_t w = w0; w <= w1; ++w) {
-            const float *x = part_of(w);
-            const float f = __builtin_amdgcn_exp2f(x[rr] - ms);
-            l += x[C::ROWS + rr] * f;
-            o += *(const floatx4 *)(x + 2 * C::ROWS + rr * C::DP + d) * f;
-        }
-        const int r = rt * C::ROWS + rr, t = r / p.group, g = r - t * p.group;
-        const int64_t at = ((int64_t)b * p.T + t) * p.Hq + hk * p.group + g;
-        const bool some = !(l <= 0.0f);
-        const float f = some ? (C::E4M3 && p.c.v_scale ? p.c.v_scale[hk] : 1.0f) / l : 0.0f;
-        if (d < p.D) {
-            bf16x2 y[2];
+    constexpr int TR = C::DP / 4, NR = 256 / TR, N = 8;
+    const int32_t *const join = p.join + blockIdx.x * kJoinWords;
+    const int b = join[0];
+    if (b < 0) return;
+    const int hk = join[1], rt = join[2], w0 = join[3], w1 = join[4], n = join[5];
+    const int rr = blockIdx.y * NR + threadIdx.x / TR, d = (threadIdx.x % TR) * 4;
+    const int r = rt * C::ROWS + rr;
+    if (r >= n * p.group) return;
+    float m = -__builtin_inff(), l = 0.0f;
+    floatx4 o = {0, 0, 0, 0};
+    for (int w = w0; w <= w1; w += N) {
+        float pm[N], pl[N];
+        floatx4 po[N];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e >> 1][e & 1] = (__bf16)(some ? o[e] * f : 0.0f);
-            *(uint2 *)(p.out + at * p.D + d) = __builtin_bit_cast(uint2, y);
+        for (int k = 0; k < N; ++k) {
+            // the first share begins the tile (part 1), in the others it is what they begin with (part 0)
+            const int v = w + k <= w1 ? w + k : w1;
+            const float *x = p.part + (int64_t)(v * 2 + (v == w0)) * C::PART;
+            pm[k] = w + k <= w1 ? x[rr] : -__builtin_inff();
+            pl[k] = x[C::ROWS + rr];
+            po[k] = *(const floatx4 *)(x + 2 * C::ROWS + rr * C::DP + d);
         }
-        if (p.lse && d == 0)
-            p.lse[at] = some ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f : -__builtin_inff();
+        float mn = m;
+#pragma unroll
+        for (int k = 0; k < N; ++k) mn = fmaxf(mn, pm[k]);
+        const float ms = mn == -__builtin_inff() ? 0.0f : mn;
+        const float f0 = __builtin_amdgcn_exp2f(m - ms);
+        l *= f0;
+        o *= f0;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if (w + k > w1) continue;
+            const float f = __builtin_amdgcn_exp2f(pm[k] - ms);
+            l += pl[k] * f;
+            o += po[k] * f;
+        }
+        m = mn;
     }
+    const int t = r / p.group, g = r - t * p.group;
+    const int64_t at = ((int64_t)b * p.T + t) * p.Hq + hk * p.group + g;
+    const bool some = !(l <= 0.0f);
+    const float f = some ? (C::E4M3 && p.c.v_scale ? p.c.v_scale[hk] : 1.0f) / l : 0.0f;
+    if (d < p.D) {
+        bf16x2 y[2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e >> 1][e & 1] = (__bf16)(some ? o[e] * f : 0.0f);
+        *(uint2 *)(p.out + at * p.D + d) = __builtin_bit_cast(uint2, y);
+    }
+    if (p.lse && d == 0) p.lse[at] = some ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f : -__builtin_inff();
 }
 
 }  // namespace dsel
