@@ -1250,15 +1250,20 @@ AttnKernels attn_kernels() {
 }
 template <bool E4M3>
 AttnKernels attn_pick(int64_t rows, int64_t dim) {
-    const int rw = rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
+    constexpr int S = E4M3 ? 64 : 32;
     if (dim <= 64)
-        return rw == 1 ? attn_kernels<AttnCfg<E4M3, 64, 1, 4, 32>>()
-             : rw == 2 ? attn_kernels<AttnCfg<E4M3, 64, 2, 2, E4M3 ? 64 : 32>>() : attn_kernels<AttnCfg<E4M3, 64, 4, 1, 64>>();
+        return rows <= 32           ? attn_kernels<AttnCfg<E4M3, 64, 1, 1, 4, 32, 2>>()
+               : rows <= 64         ? attn_kernels<AttnCfg<E4M3, 64, 2, 1, 2, S, 2>>()
+               : rows <= 128 || E4M3 ? attn_kernels<AttnCfg<E4M3, 64, 4, 1, 1, 64, 2>>()
+                                    : attn_kernels<AttnCfg<E4M3, 64, E4M3 ? 4 : 8, 1, 1, 64, 2>>();
     if (dim <= 128)
-        return rw == 1 ? attn_kernels<AttnCfg<E4M3, 128, 1, 4, 32>>()
-             : rw == 2 ? attn_kernels<AttnCfg<E4M3, 128, 2, 2, E4M3 ? 64 : 32>>() : attn_kernels<AttnCfg<E4M3, 128, 4, 1, 64>>();
-    return rw == 1 ? attn_kernels<AttnCfg<E4M3, 256, 1, 2, 32>>()
-         : rw == 2 ? attn_kernels<AttnCfg<E4M3, 256, 2, 1, 32>>() : attn_kernels<AttnCfg<E4M3, 256, 4, 1, 32>>();
+        return rows <= 32    ? attn_kernels<AttnCfg<E4M3, 128, 1, 1, 4, 32, 2>>()
+               : rows <= 64  ? attn_kernels<AttnCfg<E4M3, 128, 2, 1, 2, S, 2>>()
+               : rows <= 128 ? attn_kernels<AttnCfg<E4M3, 128, 4, 1, 1, 64, 2>>()
+                             : attn_kernels<AttnCfg<E4M3, 128, 8, 1, 1, 64, 3>>();
+    return rows <= 32   ? attn_kernels<AttnCfg<E4M3, 256, 1, 2, 2, 32, 2>>()
+           : rows <= 64 ? attn_kernels<AttnCfg<E4M3, 256, 2, 2, 1, 32, 2>>()
+                        : attn_kernels<AttnCfg<E4M3, 256, 4, 2, 1, 32, 3>>();
 }
 
 }  // namespace

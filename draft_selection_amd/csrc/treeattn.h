@@ -12,6 +12,8 @@
 // of KW groups of keys, whose sums are joined through LDS at the end.  Few rows
 // take many key groups (each wave then streams K and V of its own, with no
 // barrier), many rows take many row waves (each tile is read once for all).
+// Wide heads (256) split a row wave's output columns over CW = 2 waves, which
+// both compute the scores: the sums then leave room for q in the registers.
 //
 // Products.  S^T = K Q^T by 32 x 32 x 16 MFMA, so a lane holds scores of one row
 // (l % 32) and its softmax needs one exchange, with lane l ^ 32, for the maximum
@@ -50,20 +52,29 @@ constexpr int kJoinWords = 8;
 
 __device__ u32x4 g_attn_zero[1];  // what a key that is none reads (never written)
 
-template <bool E4M3_, int DP_, int RW_, int KW_, int KT_>
+// E4M3: 8-bit cache; DP: padded head dim; RW waves of 32 rows, each as CW waves
+// that hold DP / CW columns of the output, by KW key groups; KT keys a tile; ST
+// ring stages
+template <bool E4M3_, int DP_, int RW_, int CW_, int KW_, int KT_, int ST_>
 struct AttnCfg {
     static constexpr bool E4M3 = E4M3_;
-    static constexpr int DP = DP_, RW = RW_, KW = KW_, KT = KT_;  // padded head dim, row waves, key groups, keys a tile
-    static constexpr int RB = DP * (E4M3 ? 1 : 2), CH = RB / 16;  // bytes and 16-byte chunks of a tile row
-    static constexpr int NT = 64 * RW * KW, ROWS = 32 * RW, ROUND = KT * KW;
-    static constexpr int TILE = KT * RB, LDS = KW * 4 * TILE;  // K and V, two stages
-    static constexpr int LOADS = TILE / 1024 / RW;             // LDS-DMA loads of a wave per K or V tile
-    static constexpr int PART = ROWS * (DP + 2);               // floats of one partial result
-    // workgroups on a CU, as far as LDS allows (160 KB) and 512 registers a lane:
-    // heads of 256 need more than 256 of them
-    static constexpr int WGS = DP > 128 ? (NT == 128 && LDS <= 80 * 1024 ? 2 : 1) : LDS <= 80 * 1024 ? 2 : 1;
+    static constexpr int DP = DP_, RW = RW_, CW = CW_, KW = KW_, KT = KT_, ST = ST_;
+    static constexpr int GW = RW * CW;                          // waves of a key group
+    static constexpr int RB = DP * (E4M3 ? 1 : 2);              // bytes of a tile row
+    static constexpr int NT = 64 * GW * KW, ROWS = 32 * RW, ROUND = KT * KW;
+    static constexpr int TILE = KT * RB, GROUP = 2 * ST * TILE;  // K tiles, then V tiles of a key group
+    static constexpr int SUMS = (KW - 1) * GW * (DP / CW / 2 + 2) * 256;  // the groups' sums, in the ring's place
+    static constexpr int RING = KW * GROUP > SUMS ? KW * GROUP : SUMS;
+    static constexpr int LDS = RING + GW * KW * ST * 256;       // and page ids, per wave
+    static constexpr int LOADS = TILE / 1024 / GW;              // LDS-DMA loads of a wave per K or V tile
+    static constexpr int STEP = 2 * LOADS + 1;                  // and of a round: K, V, page ids
+    static constexpr int PART = ROWS * (DP + 2);                // floats of one partial result
+    static constexpr int NS = KT / 32, NB = DP / 32 / CW;
+    // workgroups on a CU, as far as LDS (160 KB) and registers (512 a lane) allow
+    static constexpr int WGS = LDS <= 80 * 1024 && NT <= 256 ? 2 : 1;
     static constexpr int WAVES = WGS * NT / 256 < 1 ? 1 : WGS * NT / 256;  // per SIMD
-    static_assert(LOADS * 1024 * RW == TILE && KT <= 64 && KT % 32 == 0 && DP % 32 == 0, "tile geometry");
+    static_assert(LOADS * 1024 * GW == TILE && KT <= 64 && KT % 32 == 0 && DP % 32 == 0, "tile geometry");
+    static_assert((ST - 1) * STEP < 64, "outstanding loads are counted in 6 bits");
 
     __device__ static __forceinline__ int kkey(int row) {
         return RB >= 256 ? row & 15 : RB == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
@@ -166,6 +177,17 @@ __device__ __forceinline__ bf16x8 widen_e4m3(uint32_t a, uint32_t b) {
 
 #define DSEL_LDS __attribute__((address_space(3)))
 
+// 4 bytes per lane into LDS at lds_base + 4 * lane, as lds_dma16 does 16: page
+// ids arrive like the keys, so that no wait of the compiler's for a load of its
+// own waits for the keys in flight too
+__device__ __forceinline__ void lds_dma4(const void *src, int32_t *lds_base) {
+    const uint32_t m0v = (uint32_t)(uintptr_t)(DSEL_LDS void *)lds_base;
+    asm volatile("global_load_lds_dword %1, off"
+                 :
+                 : "{m0}"(__builtin_amdgcn_readfirstlane(m0v)), "v"(src)
+                 : "memory");
+}
+
 // 8 keys (16 kk + 8 (e / 4) + 4 (l / 32) + e % 4 of the 32 from tile row `sub`
 // on) of V's column 32 mb + l % 32
 template <class C>
@@ -256,23 +278,20 @@ __device__ __forceinline__ void add_special(floatx16 &o, const char *vt, int mb,
 
 template <class C>
 struct AttnState {
-    floatx16 o[C::DP / 32];
+    floatx16 o[C::NB];
     float m, l;  // per lane: row l % 32; l: the sum over the lane's own keys
 };
-
-// One tile of KT keys for a wave's 32 rows.  `masked` (one value per wave): bit
-// j of `see` (the lane's row) says whether key j is seen; else all are.
 template <class C>
-__device__ __forceinline__ void attn_tile(AttnState<C> &a, const bf16x8 (&q)[C::DP / 16], const char *kt,
-                                          const char *vt, float c, bool masked, uint64_t see) {
-    const int l = lane_id(), h = l >> 5, r = l & 31;
-    constexpr int NS = C::KT / 32;
-    floatx16 s[NS];
+using AttnScores = floatx16[C::NS];
+
+// Scores of a tile: S^T = K Q^T
+template <class C>
+__device__ __forceinline__ void attn_scores(AttnScores<C> &s, const bf16x8 (&q)[C::DP / 16], const char *kt) {
+    const int l = lane_id(), h = l >> 5, r = l & 31, key = C::kkey(r);
 #pragma unroll
-    for (int sub = 0; sub < NS; ++sub) {
-        s[sub] = floatx16{};
+    for (int sub = 0; sub < C::NS; ++sub) {
         const char *row = kt + (sub * 32 + r) * C::RB;
-        const int key = C::kkey(r);
+        s[sub] = floatx16{};
         if constexpr (!C::E4M3) {
 #pragma unroll
             for (int ks = 0; ks < C::DP / 16; ++ks) {
@@ -289,62 +308,75 @@ __device__ __forceinline__ void attn_tile(AttnState<C> &a, const bf16x8 (&q)[C::
             }
         }
     }
-    bool special = false;
-    if (masked) {
+}
+
+// Scores that a row does not see become -inf (bit j of `see`: key j of the tile).
+template <class C>
+__device__ __forceinline__ void attn_mask(AttnScores<C> &s, uint64_t see) {
+    const int h = lane_id() >> 5;
 #pragma unroll
-        for (int sub = 0; sub < NS; ++sub) {
-            const uint32_t w = (uint32_t)(see >> (32 * sub)) >> (4 * h);
+    for (int sub = 0; sub < C::NS; ++sub) {
+        const uint32_t w = (uint32_t)(see >> (32 * sub)) >> (4 * h);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (!((w >> (8 * (i >> 2) + (i & 3))) & 1)) s[sub][i] = -__builtin_inff();
-        }
-        special = tile_special<C>(vt);
+        for (int i = 0; i < 16; ++i)
+            if (!((w >> (8 * (i >> 2) + (i & 3))) & 1)) s[sub][i] = -__builtin_inff();
     }
+}
+
+// The running maximum only moves (and the sums are only scaled) when a row's
+// scores pass it by more than 8: weights stay below 2^8, as exact as any others.
+template <class C>
+__device__ __forceinline__ void attn_rescale(AttnState<C> &a, const AttnScores<C> &s, float c) {
     float top = -__builtin_inff();
 #pragma unroll
-    for (int sub = 0; sub < NS; ++sub)
+    for (int sub = 0; sub < C::NS; ++sub)
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[sub][i]);
     top = fmaxf(top, __uint_as_float(xor_lane32<32>(__float_as_uint(top)))) * c;
-    // The running maximum only moves (and the sums are only scaled) when a row's
-    // scores pass it by more than 8: weights stay below 2^8, exact as any others.
     if (ballot(top > a.m + 8.0f)) {
         const float m = fmaxf(a.m, top);
         const float f = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(a.m - m);
 #pragma unroll
-        for (int mb = 0; mb < C::DP / 32; ++mb)
+        for (int nb = 0; nb < C::NB; ++nb)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) a.o[mb][i] *= f;
+            for (int i = 0; i < 16; ++i) a.o[nb][i] *= f;
         a.l *= f;
         a.m = m;
     }
+}
+
+// Weights of a tile, in place, and their sums.
+template <class C>
+__device__ __forceinline__ void attn_weights(AttnState<C> &a, AttnScores<C> &s, float c) {
     const float ms = a.m == -__builtin_inff() ? 0.0f : a.m;
+    float sum = 0.0f;
 #pragma unroll
-    for (int sub = 0; sub < NS; ++sub) {
-        float sum = 0.0f;
+    for (int sub = 0; sub < C::NS; ++sub)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             s[sub][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[sub][i], c, -ms));
             sum += s[sub][i];
         }
-        a.l += sum;
+    a.l += sum;
+}
+
+// O^T += V^T P^T for column blocks nb0 .. of the wave, the weights rounded to bf16
+template <class C>
+__device__ __forceinline__ void attn_values(AttnState<C> &a, const AttnScores<C> &s, const char *vt, int nb0, bool special) {
+#pragma unroll
+    for (int sub = 0; sub < C::NS; ++sub)
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             bf16x8 w;
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = (__bf16)s[sub][8 * kk + e];
 #pragma unroll
-            for (int mb = 0; mb < C::DP / 32; ++mb) {
-                bf16x8 v = v_operand<C>(vt, 32 * sub, kk, mb);
+            for (int nb = 0; nb < C::NB; ++nb) {
+                bf16x8 v = v_operand<C>(vt, 32 * sub, kk, nb0 + nb);
                 if (special) v = only_finite(v);
-                a.o[mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w, a.o[mb], 0, 0, 0);
+                a.o[nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w, a.o[nb], 0, 0, 0);
             }
         }
-    }
-    if (special) {
-#pragma unroll
-        for (int mb = 0; mb < C::DP / 32; ++mb) add_special<C>(a.o[mb], vt, mb, see);
-    }
 }
 
 // Which of the 32 keys from position `kb` on node t of row b sees, by its mask
@@ -368,7 +400,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
     __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int rw = wave % C::RW, grp = wave / C::RW, h = lane >> 5;
+    const int gw = wave % C::GW, grp = wave / C::GW, rw = gw / C::CW, nb0 = gw % C::CW * C::NB, h = lane >> 5;
     int32_t *const join = p.join + blockIdx.x * kJoinWords;
     if (threadIdx.x == 0) join[0] = -1;
     int64_t incl;
@@ -387,7 +419,8 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
     int b = attn_find<C>(p, incl, u, &before);
     AttnRow row = attn_row<C>(p, b);
 
-    char *const ring = lds + grp * 4 * C::TILE;
+    char *const kring = lds + grp * C::GROUP, *const vring = kring + C::ST * C::TILE;
+    int32_t *const ids = (int32_t *)(lds + C::RING) + wave * C::ST * 64;
     while (u < uend) {
         while (u - before >= (int64_t)row.rts * p.c.heads * row.rounds) {  // on to the next row with work
             before += (int64_t)row.rts * p.c.heads * row.rounds;
@@ -400,6 +433,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
         const int total = row.s + row.n;
         const char *const kbase = p.c.k + 16 * (hk * p.c.head_stride);
         const char *const vbase = p.c.v + 16 * (hk * p.c.head_stride);
+        const int32_t *const table = p.t.table + b * p.t.ld;
         float c = p.scale;
         bool flip = false;  // a negative scale changes q's sign, so that c stays positive
         if (C::E4M3 && p.c.k_scale) {
@@ -408,11 +442,27 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
             c = fmaxf(p.scale * fabsf(ks), 1e-37f);
         }
 
-        // the keys of a round: lane j of every wave looks up key j of its group's tile
+        // the lane's rows, and their q: eight values of every 16-deep step
+        const int rows = row.n * p.group, r = rt * C::ROWS + rw * 32 + (lane & 31);
+        const bool live = r < rows;
+        const bool idle = rt * C::ROWS + rw * 32 >= rows;  // the whole wave: it only moves keys
+        const int t = live ? r / p.group : 0, head = hk * p.group + (live ? r - t * p.group : 0);
+        const uint16_t *const qr = (const uint16_t *)p.q + b * p.sqb + t * p.sqt + head * p.sqh;
+        bf16x8 q[C::DP / 16];
+#pragma unroll
+        for (int ks = 0; ks < C::DP / 16; ++ks) {
+            const int d = C::E4M3 ? 32 * (ks >> 1) + 16 * h + 8 * (ks & 1) : 16 * ks + 8 * h;
+            u32x4 w = live && d < p.D ? *(const u32x4 *)(qr + d) : u32x4{0, 0, 0, 0};
+            if (C::E4M3 && flip) w ^= 0x80008000u;
+            q[ks] = __builtin_bit_cast(bf16x8, w);
+        }
+
+        // The keys of a round: lane j of every wave places key j of its group's
+        // tile.  A key past the end, or of a page that is none, has no place.
         auto key_pos = [&](int round) { return round * C::ROUND + grp * C::KT + (lane & (C::KT - 1)); };
-        auto page_of = [&](int round) -> int {
+        auto entry_of = [&](int round) -> const int32_t * {
             const int k = key_pos(round);
-            return round < r1 && k < total ? p.t.table[b * p.t.ld + (uint32_t)k / (uint32_t)p.c.page_size] : -1;
+            return table + (k < total ? (uint32_t)k / (uint32_t)p.c.page_size : 0);
         };
         auto offset_of = [&](int round, int page) -> int64_t {
             const int k = key_pos(round);
@@ -423,79 +473,93 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
             }
             return (int64_t)page * p.c.page_stride + (int64_t)((uint32_t)k % (uint32_t)p.c.page_size) * p.c.slot_stride;
         };
-        auto stage = [&](char *to, int64_t off) {
+        auto stage = [&](char *to, int64_t off, const char *base, bool isv) {
 #pragma unroll
             for (int j = 0; j < C::LOADS; ++j) {
-                const int at = (rw * C::LOADS + j) * 1024, byte = at + lane * 16;
+                const int pos = (gw * C::LOADS + j) * 1024, byte = pos + lane * 16;
                 const int rr = byte / C::RB, ch = (byte % C::RB) / 16;
                 const int64_t o = (int64_t)shfl_idx64((uint64_t)off, rr);
-                const int kc = ch ^ C::kkey(rr), vc = ch ^ C::vkey(rr);
-                const char *ks = o >= 0 && kc < p.c.vecs ? kbase + 16 * (o + kc) : (const char *)g_attn_zero;
-                const char *vs = o >= 0 && vc < p.c.vecs ? vbase + 16 * (o + vc) : (const char *)g_attn_zero;
-                lds_dma16(ks, (uint16_t *)(to + at));
-                lds_dma16(vs, (uint16_t *)(to + C::TILE + at));
+                const int src = ch ^ (isv ? C::vkey(rr) : C::kkey(rr));
+                lds_dma16(o >= 0 && src < p.c.vecs ? base + 16 * (o + src) : (const char *)g_attn_zero,
+                          (uint16_t *)(to + pos));
             }
         };
-        int64_t off = offset_of(r0, page_of(r0));
-        uint64_t ok = ballot(off >= 0);
-        stage(ring, off);
-        int page = page_of(r0 + 1);
-
-        // the lane's row, and its q: eight values of every 16-deep step
-        const int r = rt * C::ROWS + rw * 32 + (lane & 31);
-        const bool live = r < row.n * p.group;
-        const int t = live ? r / p.group : 0, g = live ? r - t * p.group : 0;
-        const uint16_t *qr = (const uint16_t *)p.q + b * p.sqb + t * p.sqt + (hk * p.group + g) * p.sqh;
-        bf16x8 q[C::DP / 16];
+        // Round i computes on its own keys and starts those of round i + A, whose
+        // places it reads from page ids fetched A rounds before that.
+        constexpr int A = C::ST - 1;
+        auto slot = [&](int round) { return (uint32_t)(round - r0) % C::ST; };
+        auto start = [&](int round, int64_t off) {
+            stage(kring + slot(round) * C::TILE, off, kbase, false);
+            stage(vring + slot(round) * C::TILE, off, vbase, true);
+            lds_dma4(entry_of(round + A), ids + slot(round + A) * 64);
+        };
+        uint64_t have[C::ST];  // at the top of round i: which keys of rounds i .. i + A - 1 have a place
+        {
+            int page[A];
 #pragma unroll
-        for (int ks = 0; ks < C::DP / 16; ++ks) {
-            const int d = C::E4M3 ? 32 * (ks >> 1) + 16 * h + 8 * (ks & 1) : 16 * ks + 8 * h;
-            u32x4 w = live && d < p.D ? *(const u32x4 *)(qr + d) : u32x4{0, 0, 0, 0};
-            if (C::E4M3 && flip) w ^= 0x80008000u;
-            q[ks] = __builtin_bit_cast(bf16x8, w);
+            for (int k = 0; k < A; ++k) page[k] = *entry_of(r0 + k);
+#pragma unroll
+            for (int ks = 0; ks < C::DP / 16; ++ks) asm volatile("" : "+v"(q[ks]));  // q is here before the ring starts
+#pragma unroll
+            for (int k = 0; k < A; ++k) {
+                const int64_t off = offset_of(r0 + k, page[k]);
+                have[k] = ballot(off >= 0);
+                if (r0 + k < r1) start(r0 + k, off);
+            }
+            have[A] = 0;
         }
         AttnState<C> a;
 #pragma unroll
-        for (int mb = 0; mb < C::DP / 32; ++mb) a.o[mb] = floatx16{};
+        for (int nb = 0; nb < C::NB; ++nb) a.o[nb] = floatx16{};
         a.m = -__builtin_inff();
         a.l = 0.0f;
 
+        constexpr uint64_t kAll = ~0ull >> (64 - C::KT);
         for (int round = r0; round < r1; ++round) {
-            const char *cur = ring + ((round - r0) & 1) * 2 * C::TILE;
-            // this round's keys have landed, and nobody still reads the other stage
-            wait_vmcnt_lgkm0<0>();
-            if constexpr (C::RW > 1) wg_barrier();
+            // this round's keys have landed, and nobody still reads the slots filled next
+            if (round + A <= r1) wait_vmcnt_lgkm0<(A - 1) * C::STEP>();
+            else wait_vmcnt_lgkm0<0>();
+            if constexpr (C::GW > 1) wg_barrier();
             else asm volatile("" ::: "memory");
-            const uint64_t now = ok;
-            if (round + 1 < r1) {
-                off = offset_of(round + 1, page);
-                ok = ballot(off >= 0);
-                stage(ring + ((round + 1 - r0) & 1) * 2 * C::TILE, off);
-                page = page_of(round + 2);
+            if (round + A < r1) {
+                const int64_t off = offset_of(round + A, ids[slot(round + A) * 64 + lane]);
+                have[A] = ballot(off >= 0);
+                start(round + A, off);
             }
+            const uint64_t now = have[0];
+#pragma unroll
+            for (int k = 0; k < A; ++k) have[k] = have[k + 1];
             const int kb = round * C::ROUND + grp * C::KT;
-            constexpr uint64_t kAll = ~0ull >> (64 - C::KT);
             const bool whole = kb + C::KT <= row.s && (now & kAll) == kAll;
+            if (idle || (now & kAll) == 0) continue;
             uint64_t see = now;
-            if (!whole) {
-                if ((now & kAll) == 0) continue;
+            if (!whole)
                 see &= sees_of(p, b, t, row.s, kb) | (C::KT == 64 ? (uint64_t)sees_of(p, b, t, row.s, kb + 32) << 32 : 0);
+            const char *const vt = vring + slot(round) * C::TILE;
+            AttnScores<C> s;
+            attn_scores<C>(s, q, kring + slot(round) * C::TILE);
+            if (!whole) attn_mask<C>(s, see);
+            attn_rescale<C>(a, s, c);
+            attn_weights<C>(a, s, c);
+            const bool special = !whole && tile_special<C>(vt);
+            attn_values<C>(a, s, vt, nb0, special);
+            if (special) {
+#pragma unroll
+                for (int nb = 0; nb < C::NB; ++nb) add_special<C>(a.o[nb], vt, nb0 + nb, see);
             }
-            attn_tile<C>(a, q, cur, cur + C::TILE, c, !whole, see);
         }
 
         a.l += __uint_as_float(xor_lane32<32>(__float_as_uint(a.l)));
         if constexpr (C::KW > 1) {
             // groups 1.. hand their sums to group 0, register by register
-            constexpr int N = C::DP / 2 + 2;  // floats per lane
-            static_assert((C::KW - 1) * C::RW * N * 256 <= C::LDS, "sums fit the ring");
-            float *mine = (float *)lds + ((grp - 1) * C::RW + rw) * N * 64 + lane;
+            constexpr int N = C::NB * 16 + 2;  // floats per lane
             __syncthreads();
             if (grp > 0) {
+                float *mine = (float *)lds + ((grp - 1) * C::GW + gw) * N * 64 + lane;
 #pragma unroll
-                for (int mb = 0; mb < C::DP / 32; ++mb)
+                for (int nb = 0; nb < C::NB; ++nb)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) mine[(mb * 16 + i) * 64] = a.o[mb][i];
+                    for (int i = 0; i < 16; ++i) mine[(nb * 16 + i) * 64] = a.o[nb][i];
                 mine[(N - 2) * 64] = a.m;
                 mine[(N - 1) * 64] = a.l;
             }
@@ -503,16 +567,16 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
             if (grp == 0) {
 #pragma unroll 1
                 for (int k = 0; k < C::KW - 1; ++k) {
-                    const float *from = (const float *)lds + (k * C::RW + rw) * N * 64 + lane;
+                    const float *from = (const float *)lds + (k * C::GW + gw) * N * 64 + lane;
                     const float fm = from[(N - 2) * 64], fl = from[(N - 1) * 64];
                     const float m = fmaxf(a.m, fm), ms = m == -__builtin_inff() ? 0.0f : m;
                     const float fa = __builtin_amdgcn_exp2f(a.m - ms), fb = __builtin_amdgcn_exp2f(fm - ms);
                     a.l = a.l * fa + fl * fb;
                     a.m = m;
 #pragma unroll
-                    for (int mb = 0; mb < C::DP / 32; ++mb)
+                    for (int nb = 0; nb < C::NB; ++nb)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) a.o[mb][i] = a.o[mb][i] * fa + from[(mb * 16 + i) * 64] * fb;
+                        for (int i = 0; i < 16; ++i) a.o[nb][i] = a.o[nb][i] * fa + from[(nb * 16 + i) * 64] * fb;
                 }
             }
         }
@@ -522,42 +586,41 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
             join[1] = hk;
             join[2] = rt;
             join[3] = (int)share;
-            join[4] = (int)((((u - r0) + row.rounds) * W - 1) / U);
+            join[4] = (int)(((u + row.rounds) * W - 1) / U);
             join[5] = row.n;
         }
-        if (grp == 0) {
+        if (grp == 0 && live) {
             if (r0 == 0 && r1 == row.rounds) {
+                const float vs = C::E4M3 && p.c.v_scale ? p.c.v_scale[hk] : 1.0f;
                 const bool some = !(a.l <= 0.0f);  // NaN counts as something
-                const float f = some ? (C::E4M3 && p.c.v_scale ? p.c.v_scale[hk] : 1.0f) / a.l : 0.0f;
-                if (live) {
-                    const int64_t o = (((int64_t)b * p.T + t) * p.Hq + hk * p.group + g);
+                const float f = some ? vs / a.l : 0.0f;
+                const int64_t at = ((int64_t)b * p.T + t) * p.Hq + head;
 #pragma unroll
-                    for (int mb = 0; mb < C::DP / 32; ++mb)
+                for (int nb = 0; nb < C::NB; ++nb)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int d = 32 * mb + 8 * i + 4 * h;
-                            if (d >= p.D) continue;
-                            bf16x2 y[2];
+                    for (int i = 0; i < 4; ++i) {
+                        const int d = 32 * (nb0 + nb) + 8 * i + 4 * h;
+                        if (d >= p.D) continue;
+                        bf16x2 y[2];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) y[e >> 1][e & 1] = (__bf16)(some ? a.o[mb][4 * i + e] * f : 0.0f);
-                            *(uint2 *)(p.out + o * p.D + d) = __builtin_bit_cast(uint2, y);
-                        }
-                    if (p.lse && h == 0)
-                        p.lse[o] = some ? (a.m + __builtin_amdgcn_logf(a.l)) * 0.69314718055994531f : -__builtin_inff();
-                }
+                        for (int e = 0; e < 4; ++e) y[e >> 1][e & 1] = (__bf16)(some ? a.o[nb][4 * i + e] * f : 0.0f);
+                        *(uint2 *)(p.out + at * p.D + d) = __builtin_bit_cast(uint2, y);
+                    }
+                if (p.lse && h == 0 && nb0 == 0)
+                    p.lse[at] = some ? (a.m + __builtin_amdgcn_logf(a.l)) * 0.69314718055994531f : -__builtin_inff();
             } else {
                 float *to = p.part + (share * 2 + (r0 == 0)) * C::PART;
                 const int rr = rw * 32 + (lane & 31);
-                if (h == 0) {
+                if (h == 0 && nb0 == 0) {
                     to[rr] = a.m;
                     to[C::ROWS + rr] = a.l;
                 }
 #pragma unroll
-                for (int mb = 0; mb < C::DP / 32; ++mb)
+                for (int nb = 0; nb < C::NB; ++nb)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const floatx4 y = {a.o[mb][4 * i], a.o[mb][4 * i + 1], a.o[mb][4 * i + 2], a.o[mb][4 * i + 3]};
-                        *(floatx4 *)(to + 2 * C::ROWS + rr * C::DP + 32 * mb + 8 * i + 4 * h) = y;
+                        const floatx4 y = {a.o[nb][4 * i], a.o[nb][4 * i + 1], a.o[nb][4 * i + 2], a.o[nb][4 * i + 3]};
+                        *(floatx4 *)(to + 2 * C::ROWS + rr * C::DP + 32 * (nb0 + nb) + 8 * i + 4 * h) = y;
                     }
             }
         }
