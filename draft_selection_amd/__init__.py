@@ -38,6 +38,7 @@ import ctypes as C
 import functools
 import inspect
 import os
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -135,14 +136,15 @@ def _load():
             "dsel_verify": ([P, I32, I64, I64, P, I64, I64, P, P, P, I32, C.c_float, P, P, P, P, P, SZ, P], I32),
             "dsel_tree_mask": ([P, I64, I64, P, P, P, P], I32),
             "dsel_tree_attn_workspace_bytes": ([I64, I64, I64, I64, I64], SZ),
-            "dsel_tree_attn": ([C.POINTER(TreeAttnArgs), C.POINTER(CacheArgs), P, SZ, P], I32),
+            # structures by address: a ctypes one (byref) or its packed bytes
+            "dsel_tree_attn": ([P, P, P, SZ, P], I32),
             "dsel_tree_accept": ([P, P, P, I64, I64, I64, P, P, P, P, P], I32),
-            "dsel_cache_append": ([P, P, C.POINTER(I64), C.POINTER(CacheArgs), P, I64, I64, P, I64, I64, P, P], I32),
-            "dsel_cache_compact": ([C.POINTER(CacheArgs), P, I64, I64, P, P, P, I64, I64, P, P], I32),
-            "dsel_pages_reserve": ([C.POINTER(PagesArgs), P, P, P], I32),
+            "dsel_cache_append": ([P, P, P, P, P, I64, I64, P, I64, I64, P, P], I32),
+            "dsel_cache_compact": ([P, P, I64, I64, P, P, P, I64, I64, P, P], I32),
+            "dsel_pages_reserve": ([P, P, P, P], I32),
             "dsel_pages_fork_workspace_bytes": ([I64], SZ),
-            "dsel_pages_fork": ([C.POINTER(PagesArgs), P, C.POINTER(CacheArgs), P, P, SZ, P], I32),
-            "dsel_pages_free": ([C.POINTER(PagesArgs), P, P], I32),
+            "dsel_pages_fork": ([P, P, P, P, P, SZ, P], I32),
+            "dsel_pages_free": ([P, P, P], I32),
             "dsel_device_error": ([C.POINTER(C.c_int32), P], I32),
             "dsel_status_string": ([I32], C.c_char_p),
             "dsel_version": ([], I32),
@@ -721,6 +723,17 @@ class Pages(NamedTuple):
     page_size: int
 
 
+# The calls below are made many times per step on small tensors, where their host
+# time counts: arguments travel as packed bytes (the layouts of the ctypes
+# structures above, which cost several times as much to fill) and checks look at
+# each attribute once.
+_PACK_CACHE = struct.Struct("@PPi4x9qPP").pack
+_PACK_ATTN = struct.Struct("@P6qPPqqPPf4xPP").pack
+_PACK_PAGES = struct.Struct("@PqqqPPPqq").pack
+_PACK_STRIDES = struct.Struct("@4q").pack
+_I32, _F32, _BF16, _E4M3 = torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn
+
+
 def _placed(fn):
     """Run ``fn`` on its first argument's device and on ``stream`` (default: that
     device's current stream), both made current, so that what it allocates
@@ -736,7 +749,7 @@ def _placed(fn):
                 raise ValueError(f"{fn.__name__}: stream is of {stream.device}, the tensors are on {t.device}")
             with torch.cuda.stream(stream):
                 return fn(first, *args, **kwargs)
-        if t.device.index != torch.cuda.current_device():
+        if t.get_device() != torch.cuda.current_device():
             with torch.cuda.device(t.device):
                 return fn(first, *args, **kwargs)
         return fn(first, *args, **kwargs)
@@ -745,64 +758,68 @@ def _placed(fn):
 
 
 def _on(dev, t, name, dtype, shape=None):
-    _need(t, name, dtype, shape)
-    if t.device != dev:
+    """A contiguous tensor of this type and shape on ``dev``; its address."""
+    if t.dtype is not dtype or t.device != dev or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        _need(t, name, dtype, shape)
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return t.data_ptr()
 
 
 def _lens_on(dev, block_len, B):
-    if block_len is None:
-        return None
-    _on(dev, block_len, "block_len", torch.int32, (B,))
-    return block_len.data_ptr()
+    return 0 if block_len is None else _on(dev, block_len, "block_len", _I32, (B,))
 
 
 def _table(dev, page_table, seq_len, B):
-    """Checked ``(row stride, pages per row)`` of a page table ``[B, max_pages]``
-    with unit stride inside a row."""
-    if page_table.device != dev or page_table.dtype != torch.int32:
+    """Checked ``(address, row stride, pages per row, address of seq_len)`` of a
+    page table ``[B, max_pages]`` with unit stride inside a row."""
+    if page_table.device != dev or page_table.dtype is not _I32:
         raise TypeError(f"page_table must be int32 on {dev}")
-    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.shape[1] < 1:
+    shape = page_table.shape
+    if len(shape) != 2 or shape[0] != B or shape[1] < 1:
         raise ValueError(f"page_table must be [{B}, max_pages]")
-    n = page_table.shape[1]
-    ld = page_table.stride(0) if B > 1 else n
-    if (n > 1 and page_table.stride(1) != 1) or ld < n:
+    n = shape[1]
+    ld, one = page_table.stride()
+    if B <= 1:
+        ld = n
+    if (n > 1 and one != 1) or ld < n:
         raise ValueError("page_table must have unit stride in its rows")
-    _on(dev, seq_len, "seq_len", torch.int32, (B,))
-    return ld, n
+    return page_table.data_ptr(), ld, n, _on(dev, seq_len, "seq_len", _I32, (B,))
 
 
-def _cache(dev, k, v, k_scale=None, v_scale=None) -> CacheArgs:
-    """Arguments of a cache ``[num_pages, page_size, heads, dim]`` or ``[layers,
-    num_pages, page_size, heads, dim]``: any strides (the same for K and V), the
-    last one 1."""
-    if k.shape != v.shape or k.dim() not in (4, 5):
+def _differ(shape, a, b):
+    return a != b and any(n > 1 and x != y for n, x, y in zip(shape, a, b))
+
+
+def _cache(dev, k, v, k_scale=None, v_scale=None):
+    """Packed arguments and ``(layers, pages, page_size, heads, dim)`` of a cache
+    ``[num_pages, page_size, heads, dim]`` or ``[layers, num_pages, page_size,
+    heads, dim]``: any strides (the same for K and V), the last one 1."""
+    shape, sk, dt = k.shape, k.stride(), k.dtype
+    if v.shape != shape or len(shape) not in (4, 5):
         raise ValueError("k_cache and v_cache must be [layers,] [num_pages, page_size, heads, dim] alike")
-    if k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+    if v.dtype is not dt or (dt is not _BF16 and dt is not _E4M3):
         raise TypeError("k_cache and v_cache must both be bfloat16 or float8_e4m3fn")
     if k.device != dev or v.device != dev:
         raise ValueError(f"the caches must be on {dev}")
-    shape, sk, sv = k.shape, k.stride(), v.stride()
-    if sk[-1] != 1 or sv[-1] != 1:
-        raise ValueError("the caches need unit stride in the last dim")
-    if sk != sv and any(n > 1 and a != b for n, a, b in zip(shape, sk, sv)):
-        raise ValueError("k_cache and v_cache must have the same strides")
-    if k.dim() == 4:
-        shape, sk = (1,) + tuple(shape), (0,) + tuple(sk)
+    if sk[-1] != 1 or _differ(shape, sk, v.stride()):
+        raise ValueError("k_cache and v_cache must have the same strides, the last one 1")
+    if len(shape) == 4:
+        shape, sk, heads = (1, *shape), (0, *sk), (shape[2],)
+    else:
+        heads = (shape[0], shape[3])
+    ps = [0, 0]
+    for i, t in enumerate((k_scale, v_scale)):
+        if t is not None:
+            if dt is not _E4M3:
+                raise ValueError("k_scale and v_scale are for float8_e4m3fn caches")
+            ps[i] = _on(dev, t, "v_scale" if i else "k_scale", _F32, heads)
     L, N, P, H, D = shape
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t is None:
-            continue
-        if k.dtype != torch.float8_e4m3fn:
-            raise ValueError(f"{n} is for float8_e4m3fn caches")
-        _on(dev, t, n, torch.float32, (H,) if k.dim() == 4 else (L, H))
-    return CacheArgs(k.data_ptr(), v.data_ptr(), BF16 if k.dtype == torch.bfloat16 else E4M3, L, sk[0], N, sk[1], P,
-                     sk[2], H, sk[3], D, k_scale.data_ptr() if k_scale is not None else None,
-                     v_scale.data_ptr() if v_scale is not None else None)
+    return _PACK_CACHE(k.data_ptr(), v.data_ptr(), BF16 if dt is _BF16 else E4M3, L, sk[0], N, sk[1], P, sk[2], H, sk[3],
+                       D, *ps), shape
 
 
-def _cur():
-    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+def _cur(dev):
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 @_placed
@@ -814,16 +831,16 @@ def tree_mask(parent, block_len=None, out=None):
     int32.  Nodes past ``block_len`` are not written."""
     B, T = parent.shape
     dev = parent.device
-    _on(dev, parent, "parent", torch.int32)
+    pp = _on(dev, parent, "parent", _I32)
     if out is None:
-        mask = torch.empty((B, T, (T + 31) // 32), dtype=torch.int32, device=dev)
-        depth = torch.empty((B, T), dtype=torch.int32, device=dev)
+        mask = torch.empty((B, T, (T + 31) // 32), dtype=_I32, device=dev)
+        depth = torch.empty((B, T), dtype=_I32, device=dev)
+        pm, pd = mask.data_ptr(), depth.data_ptr()
     else:
         mask, depth = out
-        _on(dev, mask, "mask", torch.int32, (B, T, (T + 31) // 32))
-        _on(dev, depth, "depth", torch.int32, (B, T))
-    _check(_load().dsel_tree_mask(parent.data_ptr(), B, T, _lens_on(dev, block_len, B), mask.data_ptr(),
-                                  depth.data_ptr(), _cur()), "dsel_tree_mask")
+        pm = _on(dev, mask, "mask", _I32, (B, T, (T + 31) // 32))
+        pd = _on(dev, depth, "depth", _I32, (B, T))
+    _check(_load().dsel_tree_mask(pp, B, T, _lens_on(dev, block_len, B), pm, pd, _cur(dev)), "dsel_tree_mask")
     return mask, depth
 
 
@@ -845,40 +862,38 @@ def tree_attn(q, k_cache, v_cache, page_table, seq_len, mask=None, block_len=Non
     ``mask`` (tree_mask's layout; None: those up to itself).  ``scale`` defaults
     to ``dim ** -0.5``.  Returns ``(out [B, T, q_heads, dim] bf16, lse [B, T,
     q_heads] fp32 or None)``; a token that sees nothing gets 0 and -inf."""
-    if q.dim() != 4 or q.dtype != torch.bfloat16:
+    shape, sq, dev = q.shape, q.stride(), q.device
+    if len(shape) != 4 or q.dtype is not _BF16:
         raise TypeError("q must be bfloat16 [B, T, q_heads, dim]")
-    B, T, Hq, D = q.shape
-    dev = q.device
-    if q.stride(3) != 1 and D > 1:
+    B, T, Hq, D = shape
+    if sq[3] != 1 and D > 1:
         raise ValueError("q must have unit stride in the last dim")
     if k_cache.dim() != 4:
         raise ValueError("tree_attn takes one layer's cache [num_pages, page_size, heads, dim]")
-    c = _cache(dev, k_cache, v_cache, k_scale, v_scale)
-    if c.dim != D:
-        raise ValueError(f"q has head dim {D}, the cache {c.dim}")
-    ld, n = _table(dev, page_table, seq_len, B)
-    if mask is not None:
-        _on(dev, mask, "mask", torch.int32, (B, T, (T + 31) // 32))
+    cache, cs = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    if cs[4] != D:
+        raise ValueError(f"q has head dim {D}, the cache {cs[4]}")
+    pt, ld, n, ps = _table(dev, page_table, seq_len, B)
+    pm = 0 if mask is None else _on(dev, mask, "mask", _I32, (B, T, (T + 31) // 32))
     if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(shape, dtype=_BF16, device=dev)
+        po = out.data_ptr()
     else:
-        _on(dev, out, "out", torch.bfloat16, (B, T, Hq, D))
+        po = _on(dev, out, "out", _BF16, shape)
+    pl = 0
     if lse is not None:
-        _on(dev, lse, "lse", torch.float32, (B, T, Hq))
+        pl = _on(dev, lse, "lse", _F32, (B, T, Hq))
     elif want_lse:
-        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev)
-    need = tree_attn_workspace_bytes(B, T, Hq, c.heads, D)
+        lse = torch.empty((B, T, Hq), dtype=_F32, device=dev)
+        pl = lse.data_ptr()
+    lib = _load()
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(lib.dsel_tree_attn_workspace_bytes(B, T, Hq, cs[3], D), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {dev}")
-    sq = q.stride()
-    a = TreeAttnArgs(q.data_ptr(), sq[0], sq[1], sq[2], B, T, Hq, _lens_on(dev, block_len, B), page_table.data_ptr(),
-                     ld, n, seq_len.data_ptr(), mask.data_ptr() if mask is not None else None,
-                     float(D ** -0.5 if scale is None else scale), out.data_ptr(),
-                     lse.data_ptr() if lse is not None else None)
-    _check(_load().dsel_tree_attn(C.byref(a), C.byref(c), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _cur()), "dsel_tree_attn")
+    a = _PACK_ATTN(q.data_ptr(), sq[0], sq[1], sq[2], B, T, Hq, _lens_on(dev, block_len, B), pt, ld, n, ps, pm,
+                   D ** -0.5 if scale is None else scale, po, pl)
+    _check(lib.dsel_tree_attn(a, cache, workspace.data_ptr(), workspace.nbytes, _cur(dev)), "dsel_tree_attn")
     return out, lse
 
 
@@ -891,21 +906,21 @@ def tree_accept(parent, tok, target_tok, block_len=None):
     greedy verification).  Returns ``n_keep [B]`` (kept nodes, the verified one
     included), ``path [B, T]`` (their indices, -1 behind) and ``out_tok [B, T]``
     (the accepted tokens and the target's own next one, -1 behind)."""
-    B, T = parent.shape
-    dev = parent.device
-    _on(dev, parent, "parent", torch.int32)
-    _on(dev, tok, "tok", torch.int32, (B, T))
-    if target_tok.dtype != torch.int32 or target_tok.device != dev or tuple(target_tok.shape) != (B, T):
+    shape, dev = parent.shape, parent.device
+    B, T = shape
+    pp, pt = _on(dev, parent, "parent", _I32), _on(dev, tok, "tok", _I32, shape)
+    if target_tok.dtype is not _I32 or target_tok.device != dev or target_tok.shape != shape:
         raise TypeError(f"target_tok must be int32 [{B}, {T}] on {dev}")
-    step = target_tok.stride(1) if T > 1 else target_tok.stride(0) if B > 1 else 1
-    if step < 1 or (B > 1 and target_tok.stride(0) != T * step):
+    sb, st = target_tok.stride()
+    step = st if T > 1 else sb if B > 1 else 1
+    if step < 1 or (B > 1 and sb != T * step):
         raise ValueError("target_tok must be evenly spaced")
-    n_keep = torch.empty(B, dtype=torch.int32, device=dev)
-    path = torch.empty((B, T), dtype=torch.int32, device=dev)
-    out_tok = torch.empty((B, T), dtype=torch.int32, device=dev)
-    _check(_load().dsel_tree_accept(parent.data_ptr(), tok.data_ptr(), target_tok.data_ptr(), step, B, T,
-                                    _lens_on(dev, block_len, B), n_keep.data_ptr(), path.data_ptr(),
-                                    out_tok.data_ptr(), _cur()), "dsel_tree_accept")
+    n_keep = torch.empty(B, dtype=_I32, device=dev)
+    path = torch.empty(shape, dtype=_I32, device=dev)
+    out_tok = torch.empty(shape, dtype=_I32, device=dev)
+    _check(_load().dsel_tree_accept(pp, pt, target_tok.data_ptr(), step, B, T, _lens_on(dev, block_len, B),
+                                    n_keep.data_ptr(), path.data_ptr(), out_tok.data_ptr(), _cur(dev)),
+           "dsel_tree_accept")
     return n_keep, path, out_tok
 
 
@@ -916,26 +931,24 @@ def cache_append(k_new, v_new, k_cache, v_cache, page_table, seq_len, block_len=
     one layer, ``[layers, B, T, heads, dim]`` for one of several (any strides, the
     same for both, the last one 1).  float8_e4m3fn caches take ``x / scale``, held
     to +-448.  ``seq_len`` is not changed."""
-    dev = k_new.device
-    c = _cache(dev, k_cache, v_cache, k_scale, v_scale)
-    if k_new.dim() != k_cache.dim() or k_new.shape != v_new.shape:
+    shape, sk, dev = k_new.shape, k_new.stride(), k_new.device
+    cache, cs = _cache(dev, k_cache, v_cache, k_scale, v_scale)
+    if len(shape) != k_cache.dim() or v_new.shape != shape:
         raise ValueError("k_new and v_new must be [layers,] [B, T, heads, dim] as the cache")
-    if k_new.dtype != torch.bfloat16 or v_new.dtype != torch.bfloat16:
+    if k_new.dtype is not _BF16 or v_new.dtype is not _BF16:
         raise TypeError("k_new and v_new must be bfloat16")
     if v_new.device != dev:
         raise ValueError(f"v_new is on {v_new.device}, expected {dev}")
-    shape, sk, sv = k_new.shape, k_new.stride(), v_new.stride()
-    if sk[-1] != 1 or sv[-1] != 1 or (sk != sv and any(n > 1 and a != b for n, a, b in zip(shape, sk, sv))):
+    if sk[-1] != 1 or _differ(shape, sk, v_new.stride()):
         raise ValueError("k_new and v_new must have the same strides, the last one 1")
     if len(shape) == 4:
-        shape, sk = (1,) + tuple(shape), (0,) + tuple(sk)
+        shape, sk = (1, *shape), (0, *sk)
     L, B, T, H, D = shape
-    if (L, H, D) != (c.layers, c.heads, c.dim):
-        raise ValueError(f"new rows of {(L, H, D)} (layers, heads, dim), the cache has {(c.layers, c.heads, c.dim)}")
-    ld, n = _table(dev, page_table, seq_len, B)
-    _check(_load().dsel_cache_append(k_new.data_ptr(), v_new.data_ptr(), (C.c_int64 * 4)(*sk[:4]), C.byref(c),
-                                     page_table.data_ptr(), ld, n, seq_len.data_ptr(), B, T,
-                                     _lens_on(dev, block_len, B), _cur()), "dsel_cache_append")
+    if (L, H, D) != (cs[0], cs[3], cs[4]):
+        raise ValueError(f"new rows of {(L, H, D)} (layers, heads, dim), the cache has {(cs[0], cs[3], cs[4])}")
+    pt, ld, n, ps = _table(dev, page_table, seq_len, B)
+    _check(_load().dsel_cache_append(k_new.data_ptr(), v_new.data_ptr(), _PACK_STRIDES(*sk[:4]), cache, pt, ld, n, ps, B,
+                                     T, _lens_on(dev, block_len, B), _cur(dev)), "dsel_cache_append")
 
 
 @_placed
@@ -944,28 +957,25 @@ def cache_compact(k_cache, v_cache, page_table, seq_len, path, n_keep, new_len=N
     + path[b, i]`` move to ``seq_len[b] + i`` for ``i < n_keep[b]`` (path ascends, as
     tree_accept gives it).  Returns ``new_len [B]`` int32, the rows' new lengths."""
     dev = k_cache.device
-    c = _cache(dev, k_cache, v_cache)
+    cache, _ = _cache(dev, k_cache, v_cache)
     B, T = path.shape
-    _on(dev, path, "path", torch.int32)
-    _on(dev, n_keep, "n_keep", torch.int32, (B,))
-    ld, n = _table(dev, page_table, seq_len, B)
+    pp, pn = _on(dev, path, "path", _I32), _on(dev, n_keep, "n_keep", _I32, (B,))
+    pt, ld, n, ps = _table(dev, page_table, seq_len, B)
     if new_len is None:
-        new_len = torch.empty(B, dtype=torch.int32, device=dev)
-    _on(dev, new_len, "new_len", torch.int32, (B,))
-    _check(_load().dsel_cache_compact(C.byref(c), page_table.data_ptr(), ld, n, seq_len.data_ptr(), path.data_ptr(),
-                                      n_keep.data_ptr(), B, T, new_len.data_ptr(), _cur()), "dsel_cache_compact")
+        new_len = torch.empty(B, dtype=_I32, device=dev)
+    _check(_load().dsel_cache_compact(cache, pt, ld, n, ps, pp, pn, B, T, _on(dev, new_len, "new_len", _I32, (B,)),
+                                      _cur(dev)), "dsel_cache_compact")
     return new_len
 
 
-def _pages(p: Pages, arg, name) -> PagesArgs:
+def _pages(p: Pages, arg, name):
+    """(device, rows, packed dsel_pages, address of the per-row argument)"""
     dev = p.table.device
     R = p.table.shape[0]
-    ld, n = _table(dev, p.table, p.seq_len, R)
-    _on(dev, p.row_pages, "row_pages", torch.int32, (R,))
-    _on(dev, p.refcount, "refcount", torch.int32)
-    _on(dev, arg, name, torch.int32, (R,))
-    return PagesArgs(p.table.data_ptr(), ld, R, n, p.row_pages.data_ptr(), p.seq_len.data_ptr(),
-                     p.refcount.data_ptr(), p.refcount.numel(), p.page_size)
+    pt, ld, n, ps = _table(dev, p.table, p.seq_len, R)
+    return dev, R, _PACK_PAGES(pt, ld, R, n, _on(dev, p.row_pages, "row_pages", _I32, (R,)), ps,
+                               _on(dev, p.refcount, "refcount", _I32), p.refcount.numel(), p.page_size), \
+        _on(dev, arg, name, _I32, (R,))
 
 
 @_placed
@@ -973,10 +983,9 @@ def pages_reserve(pages: Pages, extra):
     """Gives every row the pages it lacks to hold ``seq_len[r] + extra[r]``
     positions: the lowest free ones, in row order; all rows or none.  Returns
     ``granted [1]`` int32 (0 also sets DEVERR_POOL)."""
-    a = _pages(pages, extra, "extra")
-    granted = torch.ones(1, dtype=torch.int32, device=extra.device) if a.rows == 0 else \
-        torch.empty(1, dtype=torch.int32, device=extra.device)
-    _check(_load().dsel_pages_reserve(C.byref(a), extra.data_ptr(), granted.data_ptr(), _cur()), "dsel_pages_reserve")
+    dev, R, a, px = _pages(pages, extra, "extra")
+    granted = torch.empty(1, dtype=_I32, device=dev) if R else torch.ones(1, dtype=_I32, device=dev)
+    _check(_load().dsel_pages_reserve(a, px, granted.data_ptr(), _cur(dev)), "dsel_pages_reserve")
     return granted
 
 
@@ -985,19 +994,17 @@ def pages_fork(pages: Pages, src, k_cache, v_cache):
     """Row r becomes a copy of row ``src[r]`` (-1: takes no part): whole pages
     shared, the partial last one copied in every layer; all rows or none.  Row r
     must hold no page.  Returns ``granted [1]`` int32."""
-    a = _pages(pages, src, "src")
-    dev = src.device
-    c = _cache(dev, k_cache, v_cache)
-    granted = torch.ones(1, dtype=torch.int32, device=dev) if a.rows == 0 else \
-        torch.empty(1, dtype=torch.int32, device=dev)
-    ws = torch.empty(max(a.rows, 1), dtype=torch.int32, device=dev)
-    _check(_load().dsel_pages_fork(C.byref(a), src.data_ptr(), C.byref(c), granted.data_ptr(), ws.data_ptr(),
-                                   ws.numel() * 4, _cur()), "dsel_pages_fork")
+    dev, R, a, px = _pages(pages, src, "src")
+    cache, _ = _cache(dev, k_cache, v_cache)
+    granted = torch.empty(1, dtype=_I32, device=dev) if R else torch.ones(1, dtype=_I32, device=dev)
+    ws = torch.empty(R, dtype=_I32, device=dev)  # dsel_pages_fork_workspace_bytes(R)
+    _check(_load().dsel_pages_fork(a, px, cache, granted.data_ptr(), ws.data_ptr(), 4 * R, _cur(dev)),
+           "dsel_pages_fork")
     return granted
 
 
 @_placed
 def pages_free(pages: Pages, which):
     """Rows with ``which[r] != 0`` give back every page they hold."""
-    a = _pages(pages, which, "which")
-    _check(_load().dsel_pages_free(C.byref(a), which.data_ptr(), _cur()), "dsel_pages_free")
+    dev, _, a, px = _pages(pages, which, "which")
+    _check(_load().dsel_pages_free(a, px, _cur(dev)), "dsel_pages_free")

@@ -46,7 +46,7 @@ def test_cache_geometry_is_checked(lib, kw, code):
     if c.layers == 1:
         assert _attn(lib, c) == code
     st = (C.c_int64 * 4)(0, 9 * 1024, 1024, 128)
-    assert lib.dsel_cache_append(F, F, st, C.byref(c), F, 4, 4, F, 2, 9, None, None) == code
+    assert lib.dsel_cache_append(F, F, C.byref(st), C.byref(c), F, 4, 4, F, 2, 9, None, None) == code
     assert lib.dsel_cache_compact(C.byref(c), F, 4, 4, F, F, F, 2, 9, F + 64, None) == code
     p = ds.PagesArgs(F, 4, 2, 4, F, F, F, 10, 16)
     assert lib.dsel_pages_fork(C.byref(p), F, C.byref(c), F, F, 1 << 20, None) == code
