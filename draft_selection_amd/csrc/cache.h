@@ -243,6 +243,8 @@ __global__ __launch_bounds__(1024) void pool_give_kernel(PoolParams p) {
     __shared__ int part[17];
     const int tid = threadIdx.x;
     constexpr int R = kMaxRows / 1024;
+    constexpr int64_t kPass = 1024 * 16;
+    uint32_t bits = free_bits(p, tid * 16);  // the first pass's loads fly beside the rows'
     int need[R], code[R], sum = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -284,13 +286,11 @@ __global__ __launch_bounds__(1024) void pool_give_kernel(PoolParams p) {
         at += need[i];
     }
     // does the pool hold enough?  (a pool of one pass is looked at once, below)
-    constexpr int64_t kPass = 1024 * 16;
     const bool one = p.num_pages <= kPass;
     int found = 0;
-    uint32_t bits = 0;
     int rank = 0;
     for (int64_t base = 0; base < p.num_pages && found < total; base += kPass) {
-        bits = free_bits(p, base + tid * 16);
+        if (base) bits = free_bits(p, base + tid * 16);
         int here;
         rank = block_scan1024(__builtin_popcount(bits), part, &here);
         found += here;

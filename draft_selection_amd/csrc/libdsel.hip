@@ -1246,7 +1246,7 @@ struct AttnKernels {
 template <class C>
 AttnKernels attn_kernels() {
     return {(const void *)tree_attn_kernel<C>, (const void *)tree_attn_join_kernel<C>, C::NT, C::ROWS,
-            kAttnCUs * C::WGS, C::PART, C::ROWS * C::DP / 1024};
+            kAttnCUs * C::WGS, C::PART, AttnJoin<C>::Y};
 }
 template <bool E4M3>
 AttnKernels attn_pick(int64_t rows, int64_t dim) {
@@ -1323,6 +1323,7 @@ DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cac
     p.group = (int)(a->q_heads / cache->heads);
     p.words = (int)(a->block + 31) / 32;
     p.scale = (float)((double)a->scale * 1.4426950408889634);
+    p.page_shift = (p.c.page_size & (p.c.page_size - 1)) == 0 ? __builtin_ctz((unsigned)p.c.page_size) : -1;
     p.part = (float *)workspace;
     const int64_t rows = a->block * p.group;
     const AttnKernels k = cache->dt == DSEL_E4M3 ? attn_pick<true>(rows, cache->dim) : attn_pick<false>(rows, cache->dim);

@@ -15,31 +15,50 @@ struct TreeParams {
     int32_t *n_keep, *path, *out_tok;  // tree_accept
 };
 
-// Row i of the mask holds i and every node above it.  One thread per node
-// climbs its own parent links in LDS (as many steps as the node is deep; a
-// link that does not go to an earlier node ends the climb), setting bits in its
-// own LDS words.  A launch's latency bounds it.
+// Row i of the mask holds i and every node above it.  One thread per node, and
+// links that double: after step k a node's words hold its nearest 2^k nodes
+// upwards and `up` is the node 2^k levels above, whose words and link it then
+// takes over, so a tree of 256 is done in 8 steps.  A link that goes to no
+// earlier node ends its chain.
 __global__ __launch_bounds__(kMaxTree) void tree_mask_kernel(TreeParams p) {
-    __shared__ int up[kMaxTree];
-    __shared__ uint32_t bits[kMaxTree * (kMaxTree / 32 + 1)];  // an odd stride spreads the rows over the banks
-    constexpr int S = kMaxTree / 32 + 1;
+    constexpr int W = kMaxTree / 32, S = W + 1;  // an odd stride spreads the rows over the banks
+    __shared__ int up[kMaxTree], height[kMaxTree];
+    __shared__ uint32_t bits[kMaxTree * S];
     const int b = blockIdx.x, i = threadIdx.x, words = (p.T + 31) / 32;
     const int n = block_len_of(p.len, b, p.T);
+    int a = -1, d = 0;
+    uint32_t own[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) own[w] = (i >> 5) == w ? 1u << (i & 31) : 0u;
     if (i < n) {
-        int a = p.parent[(int64_t)b * p.T + i];
+        a = p.parent[(int64_t)b * p.T + i];
         if (i == 0 ? a != -1 : (a < 0 || a >= i)) {
             device_error(kErrTree);
             a = -1;
         }
+        d = a >= 0;
+    }
+    for (int reach = 1; reach < n; reach *= 2) {
         up[i] = a;
-        for (int w = 0; w < words; ++w) bits[i * S + w] = 0;
+        height[i] = d;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            if (w < words) bits[i * S + w] = own[w];
+        __syncthreads();
+        if (a >= 0) {
+            // a node whose chain has ended keeps its height: it is the root's distance
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                if (w < words) own[w] |= bits[a * S + w];
+            d += height[a];
+            a = up[a];
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    if (i < n) {
-        int d = -1;
-        for (int a = i; a >= 0; a = up[a], ++d) bits[i * S + (a >> 5)] |= 1u << (a & 31);
-        if (p.depth) p.depth[(int64_t)b * p.T + i] = d;
-    }
+    if (i < n && p.depth) p.depth[(int64_t)b * p.T + i] = d;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+        if (w < words) bits[i * S + w] = own[w];
     __syncthreads();
     int32_t *m = p.mask + (int64_t)b * p.T * words;
     for (int e = i; e < n * words; e += blockDim.x) m[e] = (int32_t)bits[(e / words) * S + e % words];

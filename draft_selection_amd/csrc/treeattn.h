@@ -45,7 +45,8 @@ struct TreeAttnParams {
     int B, T, Hq, D, group, words;
     float scale;  // times log2(e)
     int wgs;      // workgroups that share the work
-    float *part;  // partial sums
+    int page_shift;  // log2 of the page size, -1 if it is no power of two
+    float *part;     // partial sums
     int32_t *join;  // [wgs][kJoinWords]: the row tile that begins in a workgroup's share and ends in a later one's
 };
 constexpr int kJoinWords = 8;
@@ -63,13 +64,13 @@ struct AttnCfg {
     static constexpr int RB = DP * (E4M3 ? 1 : 2);              // bytes of a tile row
     static constexpr int NT = 64 * GW * KW, ROWS = 32 * RW, ROUND = KT * KW;
     static constexpr int TILE = KT * RB, GROUP = 2 * ST * TILE;  // K tiles, then V tiles of a key group
-    static constexpr int SUMS = (KW - 1) * GW * (DP / CW / 2 + 2) * 256;  // the groups' sums, in the ring's place
+    static constexpr int SUMS = KW > 1 ? KW * GW * (DP / CW / 2 + 2) * 256 : 0;  // the groups' sums, in the ring's place
     static constexpr int RING = KW * GROUP > SUMS ? KW * GROUP : SUMS;
     static constexpr int LDS = RING + GW * KW * ST * 256;       // and page ids, per wave
     static constexpr int LOADS = TILE / 1024 / GW;              // LDS-DMA loads of a wave per K or V tile
     static constexpr int STEP = 2 * LOADS + 1;                  // and of a round: K, V, page ids
     static constexpr int PART = ROWS * (DP + 2);                // floats of one partial result
-    static constexpr int NS = KT / 32, NB = DP / 32 / CW;
+    static constexpr int NS = KT / 32, NB = DP / 32 / CW, CH = RB / 16, QUADS = NB * 4 / KW;
     // workgroups on a CU, as far as LDS (160 KB) and registers (512 a lane) allow
     static constexpr int WGS = LDS <= 80 * 1024 && NT <= 256 ? 2 : 1;
     static constexpr int WAVES = WGS * NT / 256 < 1 ? 1 : WGS * NT / 256;  // per SIMD
@@ -90,8 +91,8 @@ struct AttnCfg {
 
 // The work: units of one round (ROUND keys of one row tile), row by row of the
 // batch, within it K/V head by head, row tile by row tile, round by round;
-// workgroup w takes units [w U / W, (w + 1) U / W).  So every workgroup has the
-// same number of rounds whatever the lengths, and a tile's rounds are split
+// each workgroup takes a share of consecutive units.  So every workgroup has
+// the same number of rounds whatever the lengths, and a tile's rounds are split
 // over as many workgroups as it takes; the partial sums of a split tile are
 // joined by tree_attn_join_kernel.
 struct AttnRow {
@@ -108,12 +109,6 @@ __device__ __forceinline__ AttnRow attn_row(const TreeAttnParams &p, int64_t b) 
     r.rounds = (int)(((int64_t)r.s + r.n + C::ROUND - 1) / C::ROUND);
     return r;
 }
-template <class C>
-__device__ __forceinline__ int64_t attn_units(const TreeAttnParams &p, int64_t b) {
-    const AttnRow r = attn_row<C>(p, b);
-    return (int64_t)r.rts * p.c.heads * r.rounds;
-}
-
 __device__ __forceinline__ int64_t wave_incl_scan64(int64_t x) {
     const uint32_t lane = lane_id();
 #pragma unroll
@@ -124,44 +119,77 @@ __device__ __forceinline__ int64_t wave_incl_scan64(int64_t x) {
     return x;
 }
 
-// How many workgroups share U units: all, but none gets less than kAttnMinUnits rounds
+// Shares of U units: W of them, the first U % W one unit longer.  U passes 32
+// bits only in batches that no memory holds, but is counted in 64; 64-bit
+// division costs a wave about a microsecond and is kept off the usual path.
 constexpr int kAttnCUs = 256;
-constexpr int kAttnMinUnits = 1;
-__device__ __forceinline__ int64_t attn_shares(const TreeAttnParams &p, int64_t U) {
-    const int64_t most = (U + kAttnMinUnits - 1) / kAttnMinUnits;
-    return most < p.wgs ? most : p.wgs;
+struct AttnShares {
+    int64_t U, each, more;  // units, U / W, U % W
+    int W;
+    __device__ __forceinline__ int64_t begin(int64_t w) const { return w * each + (w < more ? w : more); }
+    __device__ __forceinline__ static int64_t div(int64_t a, int64_t b) {
+        return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+    }
+    // the share that unit u lies in
+    __device__ __forceinline__ int of(int64_t u) const {
+        const int64_t longer = more * (each + 1);
+        return (int)(u < longer ? div(u, each + 1) : more + div(u - longer, each));
+    }
+};
+__device__ __forceinline__ AttnShares attn_shares(const TreeAttnParams &p, int64_t U) {
+    AttnShares s;
+    s.U = U;
+    s.W = (int)(U < p.wgs ? U : p.wgs);
+    s.each = AttnShares::div(U, s.W);
+    s.more = U - s.each * s.W;
+    return s;
 }
 
-// The units of all rows (returned), and the row that unit u lies in with the
-// units before it.  A whole wave calls it; lane k first sums the rows of its
-// own range of ceil(B / 64).
+// The rows of the batch, 64 at a time: lane k holds row b0 + k.  A whole wave
+// calls all of this.
 template <class C>
-__device__ __forceinline__ int64_t attn_total(const TreeAttnParams &p, int64_t *mine) {
-    const int64_t c = ((int64_t)p.B + 63) / 64, b0 = lane_id() * c;
-    int64_t sum = 0;
-    for (int64_t k = 0; k < c; ++k)
-        if (b0 + k < p.B) sum += attn_units<C>(p, b0 + k);
-    const int64_t incl = wave_incl_scan64(sum);
-    *mine = incl;
-    return (int64_t)readlane64((uint64_t)incl, 63);
-}
-template <class C>
-__device__ __forceinline__ int attn_find(const TreeAttnParams &p, int64_t incl, int64_t u, int64_t *before) {
-    const int64_t c = ((int64_t)p.B + 63) / 64;
-    const int j = __builtin_ctzll(ballot(incl > u));  // u < the total, so some lane's sum passes it
-    int64_t at = j ? (int64_t)readlane64((uint64_t)incl, j - 1) : 0;
-    int64_t b = j * c;
-    if (c > 1) {
-        for (;;) {
-            const int64_t x = attn_units<C>(p, b);
-            if (at + x > u) break;
-            at += x;
-            ++b;
-        }
+struct AttnBatch {
+    int64_t incl;  // units of rows 0 .. this lane's, of the lane's range of ceil(B / 64) rows
+    AttnRow mine;  // B <= 64: the lane's row
+    __device__ __forceinline__ int64_t load(const TreeAttnParams &p) {
+        const int64_t c = ((int64_t)p.B + 63) / 64, b0 = lane_id() * c;
+        int64_t sum = 0;
+        mine = AttnRow{0, 0, 0, 0};
+        for (int64_t k = 0; k < c; ++k)
+            if (b0 + k < p.B) {
+                mine = attn_row<C>(p, b0 + k);
+                sum += (int64_t)mine.rts * p.c.heads * mine.rounds;
+            }
+        incl = wave_incl_scan64(sum);
+        return (int64_t)readlane64((uint64_t)incl, 63);
     }
-    *before = at;
-    return (int)b;
-}
+    __device__ __forceinline__ AttnRow row(const TreeAttnParams &p, int b) const {
+        if (p.B > 64) return attn_row<C>(p, b);
+        AttnRow r;
+        r.s = __builtin_amdgcn_readlane(mine.s, b);
+        r.n = __builtin_amdgcn_readlane(mine.n, b);
+        r.rts = __builtin_amdgcn_readlane(mine.rts, b);
+        r.rounds = __builtin_amdgcn_readlane(mine.rounds, b);
+        return r;
+    }
+    // the row that unit u lies in, and the units before that row
+    __device__ __forceinline__ int find(const TreeAttnParams &p, int64_t u, int64_t *before) const {
+        const int64_t c = ((int64_t)p.B + 63) / 64;
+        const int j = __builtin_ctzll(ballot(incl > u));  // u < the total, so some lane's sum passes it
+        int64_t at = j ? (int64_t)readlane64((uint64_t)incl, j - 1) : 0, b = j * c;
+        if (c > 1) {
+            for (;;) {
+                const AttnRow r = attn_row<C>(p, b);
+                const int64_t x = (int64_t)r.rts * p.c.heads * r.rounds;
+                if (at + x > u) break;
+                at += x;
+                ++b;
+            }
+        }
+        *before = at;
+        return (int)b;
+    }
+};
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
@@ -403,30 +431,30 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
     const int gw = wave % C::GW, grp = wave / C::GW, rw = gw / C::CW, nb0 = gw % C::CW * C::NB, h = lane >> 5;
     int32_t *const join = p.join + blockIdx.x * kJoinWords;
     if (threadIdx.x == 0) join[0] = -1;
-    int64_t incl;
-    const int64_t U = attn_total<C>(p, &incl);
+    AttnBatch<C> batch;
+    const int64_t U = batch.load(p);
     if (U == 0) return;
     // neighbouring shares on one XCD (workgroup i runs on XCD i % 8): row tiles
     // that read the same keys then find them in its L2
-    const int64_t W = attn_shares(p, U), per = (W + 7) >> 3;
-    if ((blockIdx.x >> 3) >= per) return;
-    const int64_t share = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (share >= W) return;
-    int64_t u = share * U / W;
-    const int64_t uend = (share + 1) * U / W;
-    if (u >= uend) return;
+    const AttnShares shares = attn_shares(p, U);
+    const int per = (shares.W + 7) >> 3;
+    if ((int)(blockIdx.x >> 3) >= per) return;
+    const int share = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if (share >= shares.W) return;
+    int64_t u = shares.begin(share);
+    const int64_t uend = shares.begin(share + 1);
     int64_t before;
-    int b = attn_find<C>(p, incl, u, &before);
-    AttnRow row = attn_row<C>(p, b);
+    int b = batch.find(p, u, &before);
+    AttnRow row = batch.row(p, b);
 
     char *const kring = lds + grp * C::GROUP, *const vring = kring + C::ST * C::TILE;
     int32_t *const ids = (int32_t *)(lds + C::RING) + wave * C::ST * 64;
     while (u < uend) {
         while (u - before >= (int64_t)row.rts * p.c.heads * row.rounds) {  // on to the next row with work
             before += (int64_t)row.rts * p.c.heads * row.rounds;
-            row = attn_row<C>(p, ++b);
+            row = batch.row(p, ++b);
         }
-        const int item = (int)((u - before) / row.rounds);
+        const int item = (int)AttnShares::div(u - before, row.rounds);
         const int r0 = (int)((u - before) - (int64_t)item * row.rounds);
         const int r1 = (int)((int64_t)row.rounds - r0 < uend - u ? row.rounds : r0 + (uend - u));
         const int hk = item / row.rts, rt = item - hk * row.rts;
@@ -458,30 +486,42 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
         }
 
         // The keys of a round: lane j of every wave places key j of its group's
-        // tile.  A key past the end, or of a page that is none, has no place.
-        auto key_pos = [&](int round) { return round * C::ROUND + grp * C::KT + (lane & (C::KT - 1)); };
+        // tile, as a byte offset.  A key past the end, or of a page that is none,
+        // has no place; it reads what the first key that has one reads, and its
+        // score is masked.
+        auto key_pos = [&](int round) { return (uint32_t)(round * C::ROUND + grp * C::KT + (lane & (C::KT - 1))); };
+        auto page_at = [&](uint32_t k) { return p.page_shift >= 0 ? k >> p.page_shift : k / (uint32_t)p.c.page_size; };
         auto entry_of = [&](int round) -> const int32_t * {
-            const int k = key_pos(round);
-            return table + (k < total ? (uint32_t)k / (uint32_t)p.c.page_size : 0);
+            const uint32_t k = key_pos(round);
+            return table + (k < (uint32_t)total ? page_at(k) : 0u);
         };
-        auto offset_of = [&](int round, int page) -> int64_t {
-            const int k = key_pos(round);
-            if (k >= total) return -1;
-            if (page < 0 || page >= p.c.num_pages) {
-                device_error(kErrPage);
-                return -1;
-            }
-            return (int64_t)page * p.c.page_stride + (int64_t)((uint32_t)k % (uint32_t)p.c.page_size) * p.c.slot_stride;
+        auto place = [&](int round, int page, uint64_t *ok) -> int64_t {
+            const uint32_t k = key_pos(round);
+            const bool in = k < (uint32_t)total, good = in && page >= 0 && page < p.c.num_pages;
+            if (in && !good) device_error(kErrPage);
+            const uint32_t slot = k - page_at(k) * (uint32_t)p.c.page_size;
+            const int64_t off = 16 * ((int64_t)page * p.c.page_stride + (int64_t)slot * p.c.slot_stride);
+            const uint64_t m = ballot(good);
+            *ok = m;
+            if (m == ~0ull) return off;
+            const int64_t first = m ? (int64_t)readlane64((uint64_t)off, __builtin_ctzll(m)) : 0;
+            return good ? off : first;
         };
-        auto stage = [&](char *to, int64_t off, const char *base, bool isv) {
+        const bool padded = p.c.vecs < C::CH;  // chunks past the head dim read zeros
+        auto stage = [&](char *kt, char *vt, int64_t off) {
 #pragma unroll
             for (int j = 0; j < C::LOADS; ++j) {
                 const int pos = (gw * C::LOADS + j) * 1024, byte = pos + lane * 16;
                 const int rr = byte / C::RB, ch = (byte % C::RB) / 16;
                 const int64_t o = (int64_t)shfl_idx64((uint64_t)off, rr);
-                const int src = ch ^ (isv ? C::vkey(rr) : C::kkey(rr));
-                lds_dma16(o >= 0 && src < p.c.vecs ? base + 16 * (o + src) : (const char *)g_attn_zero,
-                          (uint16_t *)(to + pos));
+                const int kc = ch ^ C::kkey(rr), vc = ch ^ C::vkey(rr);
+                const char *ks = kbase + 16 * kc + o, *vs = vbase + 16 * vc + o;
+                if (padded) {
+                    if (kc >= p.c.vecs) ks = (const char *)g_attn_zero;
+                    if (vc >= p.c.vecs) vs = (const char *)g_attn_zero;
+                }
+                lds_dma16(ks, (uint16_t *)(kt + pos));
+                lds_dma16(vs, (uint16_t *)(vt + pos));
             }
         };
         // Round i computes on its own keys and starts those of round i + A, whose
@@ -489,8 +529,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
         constexpr int A = C::ST - 1;
         auto slot = [&](int round) { return (uint32_t)(round - r0) % C::ST; };
         auto start = [&](int round, int64_t off) {
-            stage(kring + slot(round) * C::TILE, off, kbase, false);
-            stage(vring + slot(round) * C::TILE, off, vbase, true);
+            stage(kring + slot(round) * C::TILE, vring + slot(round) * C::TILE, off);
             lds_dma4(entry_of(round + A), ids + slot(round + A) * 64);
         };
         uint64_t have[C::ST];  // at the top of round i: which keys of rounds i .. i + A - 1 have a place
@@ -502,8 +541,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
             for (int ks = 0; ks < C::DP / 16; ++ks) asm volatile("" : "+v"(q[ks]));  // q is here before the ring starts
 #pragma unroll
             for (int k = 0; k < A; ++k) {
-                const int64_t off = offset_of(r0 + k, page[k]);
-                have[k] = ballot(off >= 0);
+                const int64_t off = place(r0 + k, page[k], &have[k]);
                 if (r0 + k < r1) start(r0 + k, off);
             }
             have[A] = 0;
@@ -522,9 +560,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
             if constexpr (C::GW > 1) wg_barrier();
             else asm volatile("" ::: "memory");
             if (round + A < r1) {
-                const int64_t off = offset_of(round + A, ids[slot(round + A) * 64 + lane]);
-                have[A] = ballot(off >= 0);
-                start(round + A, off);
+                start(round + A, place(round + A, ids[slot(round + A) * 64 + lane], &have[A]));
             }
             const uint64_t now = have[0];
 #pragma unroll
@@ -550,78 +586,84 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
         }
 
         a.l += __uint_as_float(xor_lane32<32>(__float_as_uint(a.l)));
+        floatx4 mine[C::QUADS];  // the columns that this wave writes
         if constexpr (C::KW > 1) {
-            // groups 1.. hand their sums to group 0, register by register
-            constexpr int N = C::NB * 16 + 2;  // floats per lane
+            // the key groups' sums, exchanged through LDS: every group joins (and
+            // writes) its part of the columns
+            floatx4 *const sums = (floatx4 *)lds + gw * 64 + lane;
+            float2 *const stats = (float2 *)(lds + C::KW * C::GW * C::NB * 4096) + gw * 64 + lane;
             __syncthreads();
-            if (grp > 0) {
-                float *mine = (float *)lds + ((grp - 1) * C::GW + gw) * N * 64 + lane;
 #pragma unroll
-                for (int nb = 0; nb < C::NB; ++nb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) mine[(nb * 16 + i) * 64] = a.o[nb][i];
-                mine[(N - 2) * 64] = a.m;
-                mine[(N - 1) * 64] = a.l;
-            }
+            for (int k = 0; k < C::NB * 4; ++k)
+                sums[(grp * C::NB * 4 + k) * C::GW * 64] = floatx4{a.o[k >> 2][4 * (k & 3)], a.o[k >> 2][4 * (k & 3) + 1],
+                                                                 a.o[k >> 2][4 * (k & 3) + 2], a.o[k >> 2][4 * (k & 3) + 3]};
+            stats[grp * C::GW * 64] = float2{a.m, a.l};
             __syncthreads();
-            if (grp == 0) {
-#pragma unroll 1
-                for (int k = 0; k < C::KW - 1; ++k) {
-                    const float *from = (const float *)lds + (k * C::GW + gw) * N * 64 + lane;
-                    const float fm = from[(N - 2) * 64], fl = from[(N - 1) * 64];
-                    const float m = fmaxf(a.m, fm), ms = m == -__builtin_inff() ? 0.0f : m;
-                    const float fa = __builtin_amdgcn_exp2f(a.m - ms), fb = __builtin_amdgcn_exp2f(fm - ms);
-                    a.l = a.l * fa + fl * fb;
-                    a.m = m;
+            float m = -__builtin_inff(), f[C::KW];
+            float2 st[C::KW];
 #pragma unroll
-                    for (int nb = 0; nb < C::NB; ++nb)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) a.o[nb][i] = a.o[nb][i] * fa + from[(nb * 16 + i) * 64] * fb;
-                }
+            for (int g = 0; g < C::KW; ++g) {
+                st[g] = stats[g * C::GW * 64];
+                m = fmaxf(m, st[g].x);
             }
+            const float ms = m == -__builtin_inff() ? 0.0f : m;
+            a.l = 0.0f;
+            a.m = m;
+#pragma unroll
+            for (int g = 0; g < C::KW; ++g) {
+                f[g] = __builtin_amdgcn_exp2f(st[g].x - ms);
+                a.l += st[g].y * f[g];
+            }
+#pragma unroll
+            for (int k = 0; k < C::QUADS; ++k) {
+                mine[k] = floatx4{0, 0, 0, 0};
+#pragma unroll
+                for (int g = 0; g < C::KW; ++g)
+                    mine[k] += sums[(g * C::NB * 4 + grp * C::QUADS + k) * C::GW * 64] * f[g];
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < C::QUADS; ++k)
+                mine[k] = floatx4{a.o[k >> 2][4 * (k & 3)], a.o[k >> 2][4 * (k & 3) + 1], a.o[k >> 2][4 * (k & 3) + 2],
+                                  a.o[k >> 2][4 * (k & 3) + 3]};
         }
         if (threadIdx.x == 0 && r0 == 0 && r1 < row.rounds) {
             // the tile goes on in the shares up to that of its last round
             join[0] = b;
             join[1] = hk;
             join[2] = rt;
-            join[3] = (int)share;
-            join[4] = (int)(((u + row.rounds) * W - 1) / U);
+            join[3] = share;
+            join[4] = shares.of(u + row.rounds - 1);
             join[5] = row.n;
         }
-        if (grp == 0 && live) {
+        if (live) {
+            // quad k: columns 8 k + 4 h + 0..3 of the wave's part
+            const int d0 = 32 * nb0 + 8 * (grp * C::QUADS) + 4 * h;
+            const bool first = h == 0 && nb0 == 0 && grp == 0;
             if (r0 == 0 && r1 == row.rounds) {
                 const float vs = C::E4M3 && p.c.v_scale ? p.c.v_scale[hk] : 1.0f;
                 const bool some = !(a.l <= 0.0f);  // NaN counts as something
                 const float f = some ? vs / a.l : 0.0f;
                 const int64_t at = ((int64_t)b * p.T + t) * p.Hq + head;
 #pragma unroll
-                for (int nb = 0; nb < C::NB; ++nb)
+                for (int k = 0; k < C::QUADS; ++k) {
+                    if (d0 + 8 * k >= p.D) continue;
+                    bf16x2 y[2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int d = 32 * (nb0 + nb) + 8 * i + 4 * h;
-                        if (d >= p.D) continue;
-                        bf16x2 y[2];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) y[e >> 1][e & 1] = (__bf16)(some ? a.o[nb][4 * i + e] * f : 0.0f);
-                        *(uint2 *)(p.out + at * p.D + d) = __builtin_bit_cast(uint2, y);
-                    }
-                if (p.lse && h == 0 && nb0 == 0)
+                    for (int e = 0; e < 4; ++e) y[e >> 1][e & 1] = (__bf16)(some ? mine[k][e] * f : 0.0f);
+                    *(uint2 *)(p.out + at * p.D + d0 + 8 * k) = __builtin_bit_cast(uint2, y);
+                }
+                if (p.lse && first)
                     p.lse[at] = some ? (a.m + __builtin_amdgcn_logf(a.l)) * 0.69314718055994531f : -__builtin_inff();
             } else {
-                float *to = p.part + (share * 2 + (r0 == 0)) * C::PART;
+                float *to = p.part + (int64_t)(share * 2 + (r0 == 0)) * C::PART;
                 const int rr = rw * 32 + (lane & 31);
-                if (h == 0 && nb0 == 0) {
+                if (first) {
                     to[rr] = a.m;
                     to[C::ROWS + rr] = a.l;
                 }
 #pragma unroll
-                for (int nb = 0; nb < C::NB; ++nb)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const floatx4 y = {a.o[nb][4 * i], a.o[nb][4 * i + 1], a.o[nb][4 * i + 2], a.o[nb][4 * i + 3]};
-                        *(floatx4 *)(to + 2 * C::ROWS + rr * C::DP + 32 * (nb0 + nb) + 8 * i + 4 * h) = y;
-                    }
+                for (int k = 0; k < C::QUADS; ++k) *(floatx4 *)(to + 2 * C::ROWS + rr * C::DP + d0 + 8 * k) = mine[k];
             }
         }
         u += r1 - r0;
@@ -636,15 +678,21 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
 // Joins the partial sums of the row tiles that several workgroups shared:
 // workgroup (i, y) takes 1024 / DP rows of the tile that workgroup i of the
 // attention began and did not end; a thread takes four columns of a row and has
-// the parts of eight shares in flight at a time.
+// the parts of eight shares in flight at a time.  (Four rows a thread, a quarter
+// of the workgroups: 25 us instead of 14 at 2 x 131,000 keys.)
+template <class C>
+struct AttnJoin {
+    static constexpr int TR = C::DP / 4, NR = 256 / TR, Y = C::ROWS / NR;
+};
 template <class C>
 __global__ __launch_bounds__(256) void tree_attn_join_kernel(TreeAttnParams p) {
-    constexpr int TR = C::DP / 4, NR = 256 / TR, N = 8;
+    using J = AttnJoin<C>;
+    constexpr int N = 8;
     const int32_t *const join = p.join + blockIdx.x * kJoinWords;
     const int b = join[0];
     if (b < 0) return;
     const int hk = join[1], rt = join[2], w0 = join[3], w1 = join[4], n = join[5];
-    const int rr = blockIdx.y * NR + threadIdx.x / TR, d = (threadIdx.x % TR) * 4;
+    const int rr = blockIdx.y * J::NR + threadIdx.x / J::TR, d = (threadIdx.x % J::TR) * 4;
     const int r = rt * C::ROWS + rr;
     if (r >= n * p.group) return;
     float m = -__builtin_inff(), l = 0.0f;
