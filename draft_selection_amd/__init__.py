@@ -135,7 +135,7 @@ def _load():
             "dsel_dyn_conv": ([P, P, P, P, I64, I64, P, I64, P, P, SZ, P], I32),
             "dsel_verify": ([P, I32, I64, I64, P, I64, I64, P, P, P, I32, C.c_float, P, P, P, P, P, SZ, P], I32),
             "dsel_tree_mask": ([P, I64, I64, P, P, P, P], I32),
-            "dsel_tree_attn_workspace_bytes": ([I64, I64, I64, I64, I64], SZ),
+            "dsel_tree_attn_workspace_bytes": ([I64, I64, I64, I64, I64, I32, I64], SZ),
             # structures by address: a ctypes one (byref) or its packed bytes
             "dsel_tree_attn": ([P, P, P, SZ, P], I32),
             "dsel_tree_accept": ([P, P, P, I64, I64, I64, P, P, P, P, P], I32),
@@ -844,8 +844,11 @@ def tree_mask(parent, block_len=None, out=None):
     return mask, depth
 
 
-def tree_attn_workspace_bytes(batch: int, block: int, q_heads: int, kv_heads: int, dim: int) -> int:
-    return int(_load().dsel_tree_attn_workspace_bytes(batch, block, q_heads, kv_heads, dim))
+def tree_attn_workspace_bytes(batch: int, block: int, q_heads: int, kv_heads: int, dim: int, dtype: torch.dtype,
+                              max_len: int) -> int:
+    """``dtype``: the cache's; ``max_len``: positions that a row of the page table holds."""
+    return int(_load().dsel_tree_attn_workspace_bytes(batch, block, q_heads, kv_heads, dim,
+                                                      E4M3 if dtype is _E4M3 else BF16, max_len))
 
 
 @_placed
@@ -887,13 +890,19 @@ def tree_attn(q, k_cache, v_cache, page_table, seq_len, mask=None, block_len=Non
         lse = torch.empty((B, T, Hq), dtype=_F32, device=dev)
         pl = lse.data_ptr()
     lib = _load()
+    pw = wsb = 0
     if workspace is None:
-        workspace = torch.empty(lib.dsel_tree_attn_workspace_bytes(B, T, Hq, cs[3], D), dtype=torch.uint8, device=dev)
+        wsb = lib.dsel_tree_attn_workspace_bytes(B, T, Hq, cs[3], D, BF16 if k_cache.dtype is _BF16 else E4M3, n * cs[2])
+        if wsb:
+            workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
+            pw = workspace.data_ptr()
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {dev}")
+    else:
+        pw, wsb = workspace.data_ptr(), workspace.nbytes
     a = _PACK_ATTN(q.data_ptr(), sq[0], sq[1], sq[2], B, T, Hq, _lens_on(dev, block_len, B), pt, ld, n, ps, pm,
                    D ** -0.5 if scale is None else scale, po, pl)
-    _check(lib.dsel_tree_attn(a, cache, workspace.data_ptr(), workspace.nbytes, _cur(dev)), "dsel_tree_attn")
+    _check(lib.dsel_tree_attn(a, cache, pw, wsb, _cur(dev)), "dsel_tree_attn")
     return out, lse
 
 

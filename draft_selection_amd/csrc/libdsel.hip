@@ -1269,14 +1269,13 @@ AttnKernels attn_pick(int64_t rows, int64_t dim) {
 }  // namespace
 
 DSEL_API size_t dsel_tree_attn_workspace_bytes(int64_t batch, int64_t block, int64_t q_heads, int64_t kv_heads,
-                                               int64_t dim) {
+                                               int64_t dim, dsel_dtype dt, int64_t max_len) {
     if (check_tree(batch, block) != DSEL_OK || batch == 0 || kv_heads < 1 || q_heads < 1 || q_heads > DSEL_MAX_HEADS ||
-        q_heads % kv_heads || dim < 1 || dim > DSEL_MAX_HEAD_DIM)
+        q_heads % kv_heads || dim < 1 || dim > DSEL_MAX_HEAD_DIM || (dt != DSEL_BF16 && dt != DSEL_E4M3))
         return 0;
     const int64_t rows = block * (q_heads / kv_heads);
-    const AttnKernels a = attn_pick<false>(rows, dim), b = attn_pick<true>(rows, dim);
-    const size_t na = (size_t)a.wgs * (2 * a.part + kJoinWords), nb = (size_t)b.wgs * (2 * b.part + kJoinWords);
-    return (na > nb ? na : nb) * sizeof(float);
+    const AttnKernels k = dt == DSEL_E4M3 ? attn_pick<true>(rows, dim) : attn_pick<false>(rows, dim);
+    return max_len <= kAttnWholeKeys ? 0 : (size_t)k.wgs * (2 * k.part + kJoinWords) * sizeof(float);
 }
 
 DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cache *cache, void *workspace,
@@ -1304,10 +1303,10 @@ DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cac
         if (stride[i] % 8) return DSEL_E_ALIGN;
         sq[i] = stride[i];
     }
-    if (!workspace || workspace_bytes < dsel_tree_attn_workspace_bytes(a->batch, a->block, a->q_heads, cache->heads,
-                                                                       cache->dim))
-        return DSEL_E_WORKSPACE;
-    if (!aligned(workspace, 16)) return DSEL_E_ALIGN;
+    const size_t need = dsel_tree_attn_workspace_bytes(a->batch, a->block, a->q_heads, cache->heads, cache->dim, cache->dt,
+                                                       a->max_pages * cache->page_size);
+    if (need && (!workspace || workspace_bytes < need)) return DSEL_E_WORKSPACE;
+    if (need && !aligned(workspace, 16)) return DSEL_E_ALIGN;
     p.q = (const char *)a->q;
     p.sqb = sq[0];
     p.sqt = sq[1];
@@ -1328,9 +1327,10 @@ DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cac
     const int64_t rows = a->block * p.group;
     const AttnKernels k = cache->dt == DSEL_E4M3 ? attn_pick<true>(rows, cache->dim) : attn_pick<false>(rows, cache->dim);
     p.wgs = k.wgs;
+    p.whole = need == 0;
     p.join = (int32_t *)(p.part + (int64_t)k.wgs * 2 * k.part);
     st = launch(k.attn, dim3((unsigned)k.wgs), dim3((unsigned)k.threads), &p, 0, stream);
-    if (st != DSEL_OK) return st;
+    if (st != DSEL_OK || p.whole) return st;
     return launch(k.join, dim3((unsigned)k.wgs, (unsigned)k.join_y), dim3(256), &p, 0, stream);
 }
 

@@ -45,11 +45,19 @@ struct TreeAttnParams {
     int B, T, Hq, D, group, words;
     float scale;  // times log2(e)
     int wgs;      // workgroups that share the work
+    bool whole;   // no tile is split (kAttnWholeKeys)
     int page_shift;  // log2 of the page size, -1 if it is no power of two
     float *part;     // partial sums
     int32_t *join;  // [wgs][kJoinWords]: the row tile that begins in a workgroup's share and ends in a later one's
 };
 constexpr int kJoinWords = 8;
+// Rows whose table cannot hold more keys than this are not split: a unit is a
+// whole tile, and there is no join.  One launch less for the host, and on the
+// card, whole against split (32 query heads on 8 of 128): one token over 120
+// keys 11.0 us against 12.3, over 250 12.7 against 12.5, over 500 16.4 against
+// 12.6; 8 rows of 17 nodes over 120 keys 13.8 against 16.3, over 250 18.0 against
+// 18.3.
+constexpr int kAttnWholeKeys = 256;
 
 __device__ u32x4 g_attn_zero[1];  // what a key that is none reads (never written)
 
@@ -98,6 +106,7 @@ struct AttnCfg {
 struct AttnRow {
     int s, n;        // cached positions, nodes (0: nothing to do)
     int rts, rounds; // row tiles, rounds of each
+    int units;       // units of a row tile: its rounds, or 1 (whole)
 };
 template <class C>
 __device__ __forceinline__ AttnRow attn_row(const TreeAttnParams &p, int64_t b) {
@@ -107,6 +116,7 @@ __device__ __forceinline__ AttnRow attn_row(const TreeAttnParams &p, int64_t b) 
     if (r.s < 0) r.n = r.s = 0;
     r.rts = (r.n * p.group + C::ROWS - 1) / C::ROWS;
     r.rounds = (int)(((int64_t)r.s + r.n + C::ROUND - 1) / C::ROUND);
+    r.units = p.whole && r.rounds ? 1 : r.rounds;
     return r;
 }
 __device__ __forceinline__ int64_t wave_incl_scan64(int64_t x) {
@@ -154,11 +164,11 @@ struct AttnBatch {
     __device__ __forceinline__ int64_t load(const TreeAttnParams &p) {
         const int64_t c = ((int64_t)p.B + 63) / 64, b0 = lane_id() * c;
         int64_t sum = 0;
-        mine = AttnRow{0, 0, 0, 0};
+        mine = AttnRow{0, 0, 0, 0, 0};
         for (int64_t k = 0; k < c; ++k)
             if (b0 + k < p.B) {
                 mine = attn_row<C>(p, b0 + k);
-                sum += (int64_t)mine.rts * p.c.heads * mine.rounds;
+                sum += (int64_t)mine.rts * p.c.heads * mine.units;
             }
         incl = wave_incl_scan64(sum);
         return (int64_t)readlane64((uint64_t)incl, 63);
@@ -170,6 +180,7 @@ struct AttnBatch {
         r.n = __builtin_amdgcn_readlane(mine.n, b);
         r.rts = __builtin_amdgcn_readlane(mine.rts, b);
         r.rounds = __builtin_amdgcn_readlane(mine.rounds, b);
+        r.units = __builtin_amdgcn_readlane(mine.units, b);
         return r;
     }
     // the row that unit u lies in, and the units before that row
@@ -180,7 +191,7 @@ struct AttnBatch {
         if (c > 1) {
             for (;;) {
                 const AttnRow r = attn_row<C>(p, b);
-                const int64_t x = (int64_t)r.rts * p.c.heads * r.rounds;
+                const int64_t x = (int64_t)r.rts * p.c.heads * r.units;
                 if (at + x > u) break;
                 at += x;
                 ++b;
@@ -430,7 +441,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int gw = wave % C::GW, grp = wave / C::GW, rw = gw / C::CW, nb0 = gw % C::CW * C::NB, h = lane >> 5;
     int32_t *const join = p.join + blockIdx.x * kJoinWords;
-    if (threadIdx.x == 0) join[0] = -1;
+    if (threadIdx.x == 0 && !p.whole) join[0] = -1;
     AttnBatch<C> batch;
     const int64_t U = batch.load(p);
     if (U == 0) return;
@@ -450,13 +461,13 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
     char *const kring = lds + grp * C::GROUP, *const vring = kring + C::ST * C::TILE;
     int32_t *const ids = (int32_t *)(lds + C::RING) + wave * C::ST * 64;
     while (u < uend) {
-        while (u - before >= (int64_t)row.rts * p.c.heads * row.rounds) {  // on to the next row with work
-            before += (int64_t)row.rts * p.c.heads * row.rounds;
+        while (u - before >= (int64_t)row.rts * p.c.heads * row.units) {  // on to the next row with work
+            before += (int64_t)row.rts * p.c.heads * row.units;
             row = batch.row(p, ++b);
         }
-        const int item = (int)AttnShares::div(u - before, row.rounds);
-        const int r0 = (int)((u - before) - (int64_t)item * row.rounds);
-        const int r1 = (int)((int64_t)row.rounds - r0 < uend - u ? row.rounds : r0 + (uend - u));
+        const int item = (int)AttnShares::div(u - before, row.units);
+        const int r0 = (int)((u - before) - (int64_t)item * row.units);
+        const int r1 = p.whole || (int64_t)row.rounds - r0 < uend - u ? row.rounds : (int)(r0 + (uend - u));
         const int hk = item / row.rts, rt = item - hk * row.rts;
         const int total = row.s + row.n;
         const char *const kbase = p.c.k + 16 * (hk * p.c.head_stride);
@@ -666,7 +677,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
                 for (int k = 0; k < C::QUADS; ++k) *(floatx4 *)(to + 2 * C::ROWS + rr * C::DP + d0 + 8 * k) = mine[k];
             }
         }
-        u += r1 - r0;
+        u += p.whole ? 1 : r1 - r0;
         if (u < uend) {
             // the ring (and the sums in it) are read no more
             wait_vmcnt_lgkm0<0>();

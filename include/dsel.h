@@ -541,9 +541,11 @@ dsel_status dsel_tree_mask(const int32_t *parent, int64_t batch, int64_t block, 
  * (E4M3 values are exact in bf16, the scales are applied to the fp32 sums); the
  * softmax's maximum, weights and sum are fp32; the weights are rounded to bf16
  * for their products with V, which are summed in fp32.
- *   workspace  dsel_tree_attn_workspace_bytes() bytes, 16-byte aligned;
- *              contents need no initialisation.  Calls that overlap need one
- *              each.
+ *   workspace  dsel_tree_attn_workspace_bytes() bytes, 16-byte aligned (may be
+ *              NULL when that is 0); contents need no initialisation.  Calls that
+ *              overlap need one each.  dt is the cache's type, max_len = max_pages
+ *              * page_size: a table that holds a few hundred keys per row at most
+ *              needs none, and is answered by one launch instead of two.
  * Requirements: cache->layers == 1 and cache->heads divides q_heads; q, out
  * 16-byte aligned, q's strides multiples of 8; 0 < scale < inf; table_ld >=
  * max_pages. */
@@ -560,7 +562,8 @@ typedef struct {
     uint16_t *out;
     float *lse;
 } dsel_tree_attn_args;
-size_t dsel_tree_attn_workspace_bytes(int64_t batch, int64_t block, int64_t q_heads, int64_t kv_heads, int64_t dim);
+size_t dsel_tree_attn_workspace_bytes(int64_t batch, int64_t block, int64_t q_heads, int64_t kv_heads, int64_t dim,
+                                      dsel_dtype dt, int64_t max_len);
 dsel_status dsel_tree_attn(const dsel_tree_attn_args *args, const dsel_cache *cache, void *workspace,
                            size_t workspace_bytes, dsel_stream_t stream);
 

@@ -65,11 +65,11 @@ def test_tree_attn_validation(lib):
                dict(block_len=F + 2), dict(page_table=F + 2), dict(seq_len=F + 1)):
         assert _attn(lib, **kw) == -3, kw
     assert _attn(lib, batch=0, q=None, out=None, page_table=None, seq_len=None, ws=None, wsb=0) == 0
-    need = lib.dsel_tree_attn_workspace_bytes(2, 9, 32, 8, 128)
-    if need:
-        assert _attn(lib, wsb=need - 1) == -4 and _attn(lib, ws=None) == -4 and _attn(lib, ws=F + 8) == -3
-    assert lib.dsel_tree_attn_workspace_bytes(2, 257, 32, 8, 128) == 0
-    assert lib.dsel_tree_attn_workspace_bytes(2, 9, 12, 8, 128) == 0
+    need = lambda B=2, T=9, Hq=32, H=8, D=128, dt=1, n=1 << 20: lib.dsel_tree_attn_workspace_bytes(B, T, Hq, H, D, dt, n)
+    assert need() > 0 and need(n=64) == 0 and need(T=257) == 0 and need(Hq=12) == 0 and need(dt=0) == 0 and need(D=257) == 0
+    wide = dict(table_ld=1 << 16, max_pages=1 << 16)
+    assert _attn(lib, wsb=need() - 1, **wide) == -4 and _attn(lib, ws=None, **wide) == -4
+    assert _attn(lib, ws=F + 8, **wide) == -3
 
 
 def test_tree_mask_and_accept_validation(lib):
