@@ -241,11 +241,15 @@ template <bool FORK>
 __global__ __launch_bounds__(1024) void pool_give_kernel(PoolParams p) {
     __shared__ int start[kMaxRows + 1], held[kMaxRows];
     __shared__ int part[17];
+    __shared__ unsigned long long wanted;
     const int tid = threadIdx.x;
+    if (tid == 0) wanted = 0;
+    __syncthreads();
     constexpr int R = kMaxRows / 1024;
     constexpr int64_t kPass = 1024 * 16;
     uint32_t bits = free_bits(p, tid * 16);  // the first pass's loads fly beside the rows'
-    int need[R], code[R], sum = 0;
+    int need[R], code[R];
+    int64_t sum = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int r = tid * R + i;
@@ -277,8 +281,11 @@ __global__ __launch_bounds__(1024) void pool_give_kernel(PoolParams p) {
         }
         sum += need[i];
     }
+    if (sum) atomicAdd(&wanted, (unsigned long long)sum);
     int total;
-    int at = block_scan1024(sum, part, &total);
+    int at = block_scan1024((int)sum, part, &total);
+    // more pages than 32 bits count are more than any pool holds
+    const bool many = wanted > (unsigned long long)p.num_pages;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int r = tid * R + i;
@@ -289,13 +296,13 @@ __global__ __launch_bounds__(1024) void pool_give_kernel(PoolParams p) {
     const bool one = p.num_pages <= kPass;
     int found = 0;
     int rank = 0;
-    for (int64_t base = 0; base < p.num_pages && found < total; base += kPass) {
+    for (int64_t base = 0; !many && base < p.num_pages && found < total; base += kPass) {
         if (base) bits = free_bits(p, base + tid * 16);
         int here;
         rank = block_scan1024(__builtin_popcount(bits), part, &here);
         found += here;
     }
-    const bool ok = found >= total;
+    const bool ok = !many && found >= total;
     if (tid == 0) {
         p.granted[0] = ok;
         if (!ok) device_error(kErrPool);

@@ -188,14 +188,18 @@ struct AttnBatch {
         const int64_t c = ((int64_t)p.B + 63) / 64;
         const int j = __builtin_ctzll(ballot(incl > u));  // u < the total, so some lane's sum passes it
         int64_t at = j ? (int64_t)readlane64((uint64_t)incl, j - 1) : 0, b = j * c;
-        if (c > 1) {
-            for (;;) {
-                const AttnRow r = attn_row<C>(p, b);
-                const int64_t x = (int64_t)r.rts * p.c.heads * r.units;
-                if (at + x > u) break;
-                at += x;
-                ++b;
+        // that lane's own rows, 64 at a time
+        for (int64_t k0 = 0; c > 1 && k0 < c; k0 += 64) {
+            const int64_t k = k0 + lane_id();
+            const AttnRow r = k < c && b + k < p.B ? attn_row<C>(p, b + k) : AttnRow{0, 0, 0, 0, 0};
+            const int64_t x = (int64_t)r.rts * p.c.heads * r.units, sum = wave_incl_scan64(x);
+            const uint64_t m = ballot(at + sum > u);
+            if (m) {
+                const int i = __builtin_ctzll(m);
+                *before = at + (int64_t)readlane64((uint64_t)(sum - x), i);
+                return (int)(b + k0 + i);
             }
+            at += (int64_t)readlane64((uint64_t)sum, 63);
         }
         *before = at;
         return (int)b;
@@ -478,7 +482,8 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
         if (C::E4M3 && p.c.k_scale) {
             const float ks = p.c.k_scale[hk];
             flip = ks < 0.0f;
-            c = fmaxf(p.scale * fabsf(ks), 1e-37f);
+            c = p.scale * fabsf(ks);
+            if (c == 0.0f) c = 1e-37f;  // (a score of -inf stays one)
         }
 
         // the lane's rows, and their q: eight values of every 16-deep step

@@ -278,6 +278,17 @@ def test_large_pools(dev):
             got = torch.cat([t[1, :25000], t[2, :10000]])
             assert torch.equal(got, torch.arange(n - left + 2, n - left + 2 + 35000, dtype=torch.int32, device=dev))
         assert ds.device_error() == 0
+    # wishes whose sum passes 32 bits: none is granted, nothing changes
+    rows, cols = 4000, 1 << 20
+    t = torch.full((1, cols), -1, dtype=torch.int32, device=dev).expand(rows, cols)
+    with pytest.raises(ValueError):
+        ds.pages_reserve(ds.Pages(t, ref[:1], ref[:1], ref, 1), ref[:1])  # a table of one shared row is none
+    t = torch.full((8, 1 << 29), -1, dtype=torch.int32, device=dev)
+    z = torch.zeros(8, dtype=torch.int32, device=dev)
+    p = ds.Pages(t, z.clone(), z.clone(), torch.zeros(100, dtype=torch.int32, device=dev), 1)
+    assert ds.pages_reserve(p, z + (1 << 29)).tolist() == [0] and ds.device_error() == ds.DEVERR_POOL
+    assert (p.row_pages == 0).all() and (p.refcount == 0).all() and (t[:, :4] == -1).all()
+    del t, p
     e = torch.zeros(0, dtype=torch.int32, device=dev)
     p = ds.Pages(torch.zeros((0, 2), dtype=torch.int32, device=dev), e, e, ref, 2)
     assert ds.pages_reserve(p, e).tolist() == [1]

@@ -163,6 +163,32 @@ def test_long_rows(dev, dt, D, G, T):
     _run(dev, rng, 6, T, G, 1, D, 32, ctx, dt, lens=[T, T, T, 1, T, 0], kind="random" if T == 16 else "tree")
 
 
+@pytest.mark.parametrize("B", [64, 65, 200, 777])
+def test_many_rows(dev, B):
+    """More rows than a wave has lanes, most of them short, some empty, a few long."""
+    rng = np.random.default_rng(B)
+    ctx = rng.integers(0, 60, B)
+    ctx[rng.integers(0, B, 5)] = rng.integers(500, 3000, 5)
+    lens = rng.integers(0, 3, B)
+    lens[ctx > 400] = 2
+    _run(dev, rng, B, 2, 2, 1, 64, 16, ctx, torch.bfloat16, lens=lens, kind="chain")
+
+
+@pytest.mark.parametrize("scales", [(0.0, 1.0), (-0.02, -0.5), (0.02, 0.0)])
+def test_scales_of_any_sign(dev, scales):
+    rng = np.random.default_rng(8)
+    q, a, K, V, vis, seq, n = _setup(rng, dev, 2, 6, 4, 1, 64, 16, [90, 33], torch.float8_e4m3fn)
+    old = a["k_scale"].item(), a["v_scale"].item()
+    K, V = [x * (scales[0] / old[0]) for x in K], [x * (scales[1] / old[1]) for x in V]
+    a["k_scale"].fill_(scales[0])
+    a["v_scale"].fill_(scales[1])
+    K, V = [x * (float(np.float32(scales[0])) / scales[0]) if scales[0] else x for x in K], V
+    out, lse = ds.tree_attn(q, want_lse=True, **a)
+    _check(out, lse, q, K, V, vis, seq, n, 64 ** -0.5)
+    a["k_scale"].fill_(float("nan"))
+    assert ds.tree_attn(q, **a)[0].isnan().all()
+
+
 def test_large_and_small_scores(dev):
     """Scores whose softmax is one key, and scores that are all alike."""
     rng = np.random.default_rng(3)
