@@ -924,9 +924,7 @@ def tree_accept(parent, tok, target_tok, block_len=None):
     step = st if T > 1 else sb if B > 1 else 1
     if step < 1 or (B > 1 and sb != T * step):
         raise ValueError("target_tok must be evenly spaced")
-    n_keep = torch.empty(B, dtype=_I32, device=dev)
-    path = torch.empty(shape, dtype=_I32, device=dev)
-    out_tok = torch.empty(shape, dtype=_I32, device=dev)
+    n_keep, path, out_tok = parent.new_empty(B), torch.empty_like(parent), torch.empty_like(parent)
     _check(_load().dsel_tree_accept(pp, pt, target_tok.data_ptr(), step, B, T, _lens_on(dev, block_len, B),
                                     n_keep.data_ptr(), path.data_ptr(), out_tok.data_ptr(), _cur(dev)),
            "dsel_tree_accept")
@@ -971,7 +969,7 @@ def cache_compact(k_cache, v_cache, page_table, seq_len, path, n_keep, new_len=N
     pp, pn = _on(dev, path, "path", _I32), _on(dev, n_keep, "n_keep", _I32, (B,))
     pt, ld, n, ps = _table(dev, page_table, seq_len, B)
     if new_len is None:
-        new_len = torch.empty(B, dtype=_I32, device=dev)
+        new_len = torch.empty_like(seq_len)
     _check(_load().dsel_cache_compact(cache, pt, ld, n, ps, pp, pn, B, T, _on(dev, new_len, "new_len", _I32, (B,)),
                                       _cur(dev)), "dsel_cache_compact")
     return new_len
@@ -993,7 +991,7 @@ def pages_reserve(pages: Pages, extra):
     positions: the lowest free ones, in row order; all rows or none.  Returns
     ``granted [1]`` int32 (0 also sets DEVERR_POOL)."""
     dev, R, a, px = _pages(pages, extra, "extra")
-    granted = torch.empty(1, dtype=_I32, device=dev) if R else torch.ones(1, dtype=_I32, device=dev)
+    granted = extra.new_empty(1) if R else extra.new_ones(1)
     _check(_load().dsel_pages_reserve(a, px, granted.data_ptr(), _cur(dev)), "dsel_pages_reserve")
     return granted
 
@@ -1005,8 +1003,8 @@ def pages_fork(pages: Pages, src, k_cache, v_cache):
     must hold no page.  Returns ``granted [1]`` int32."""
     dev, R, a, px = _pages(pages, src, "src")
     cache, _ = _cache(dev, k_cache, v_cache)
-    granted = torch.empty(1, dtype=_I32, device=dev) if R else torch.ones(1, dtype=_I32, device=dev)
-    ws = torch.empty(R, dtype=_I32, device=dev)  # dsel_pages_fork_workspace_bytes(R)
+    granted = src.new_empty(1) if R else src.new_ones(1)
+    ws = torch.empty_like(src)  # dsel_pages_fork_workspace_bytes(R)
     _check(_load().dsel_pages_fork(a, px, cache, granted.data_ptr(), ws.data_ptr(), 4 * R, _cur(dev)),
            "dsel_pages_fork")
     return granted
