@@ -239,59 +239,66 @@ __device__ __forceinline__ uint32_t free_bits(const PoolParams &p, int64_t first
 // that the row holds already.
 template <bool FORK>
 __global__ __launch_bounds__(1024) void pool_give_kernel(PoolParams p) {
-    __shared__ int start[kMaxRows + 1], held[kMaxRows];
-    __shared__ int part[17];
+    __shared__ int start[kMaxRows], held[kMaxRows];
+    __shared__ int part[17], over;
     __shared__ unsigned long long wanted;
     const int tid = threadIdx.x;
-    if (tid == 0) wanted = 0;
+    if (tid == 0) {
+        over = 0;
+        wanted = 0;
+    }
     __syncthreads();
     constexpr int R = kMaxRows / 1024;
     constexpr int64_t kPass = 1024 * 16;
     uint32_t bits = free_bits(p, tid * 16);  // the first pass's loads fly beside the rows'
     int need[R], code[R];
-    int64_t sum = 0;
+    // What all rows want is counted in 32 bits where that cannot overflow (1,024
+    // rows of at most 2^20 pages a scan), else also in 64.
+    const bool large = p.num_pages > (1 << 20);
+    int64_t all = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int r = tid * R + i;
         need[i] = 0;
         code[i] = -2;
-        if (r >= p.rows) continue;
-        const int have = p.row_pages[r], a = p.arg[r];
-        held[r] = have;
-        if constexpr (FORK) {
-            if (a == -1) continue;
-            bool ok = a >= 0 && a < p.rows && a != r && have == 0;
-            int n = 0;
-            if (ok) {
-                n = p.seq_len[a];
-                ok = p.arg[a] == -1 && n >= 0 && p.row_pages[a] <= p.max_pages &&
-                     (int64_t)n <= (int64_t)p.row_pages[a] * p.page_size;
+        if (i * 1024 >= p.rows) continue;  // (the same for all threads)
+        const int r = i * 1024 + tid;
+        if (r < p.rows) {
+            const int have = p.row_pages[r], a = p.arg[r];
+            held[r] = have;
+            bool bad = false;
+            if constexpr (FORK) {
+                if (a != -1) {
+                    bad = a < 0 || a >= p.rows || a == r || have != 0;
+                    if (!bad) {
+                        const int n = p.seq_len[a], h = p.row_pages[a];
+                        bad = p.arg[a] != -1 || n < 0 || h > p.max_pages || (int64_t)n > (int64_t)h * p.page_size;
+                        need[i] = !bad && n % p.page_size ? 1 : 0;
+                        code[i] = bad ? -2 : -1;
+                    }
+                }
+            } else {
+                const int n = p.seq_len[r];
+                bad = n < 0 || a < 0 || have < 0 || have > p.max_pages;
+                if (!bad) {
+                    const uint32_t keys = (uint32_t)n + (uint32_t)a, pages = keys / (uint32_t)p.page_size +
+                                                                             (keys % (uint32_t)p.page_size != 0);
+                    bad = pages > (uint32_t)p.max_pages;
+                    if (!bad) need[i] = (int)pages > have ? (int)pages - have : 0;
+                }
             }
-            if (!ok) {
-                device_error(kErrSeqLen);
-                continue;
-            }
-            need[i] = n % p.page_size ? 1 : 0;
-            code[i] = -1;
-        } else {
-            const int n = p.seq_len[r];
-            const int64_t pages = ((int64_t)n + a + p.page_size - 1) / p.page_size;
-            if (n < 0 || a < 0 || have < 0 || have > p.max_pages || pages > p.max_pages) device_error(kErrSeqLen);
-            else need[i] = pages > have ? (int)pages - have : 0;
+            if (bad) device_error(kErrSeqLen);
+            if (need[i] > p.num_pages) over = 1;
+            if (large && need[i]) atomicAdd(&wanted, (unsigned long long)need[i]);
         }
-        sum += need[i];
+        int here;
+        const int at = block_scan1024(need[i], part, &here);
+        if (r < p.rows) start[r] = (int)all + at;
+        all += here;
     }
-    if (sum) atomicAdd(&wanted, (unsigned long long)sum);
-    int total;
-    int at = block_scan1024((int)sum, part, &total);
-    // more pages than 32 bits count are more than any pool holds
-    const bool many = wanted > (unsigned long long)p.num_pages;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int r = tid * R + i;
-        if (r < p.rows) start[r] = at;
-        at += need[i];
-    }
+    __syncthreads();
+    // more pages than the pool has, and 32 bits may count, are more than it holds
+    const bool many = over || (large ? wanted > (unsigned long long)p.num_pages : all > p.num_pages);
+    const int total = (int)all;
     // does the pool hold enough?  (a pool of one pass is looked at once, below)
     const bool one = p.num_pages <= kPass;
     int found = 0;
@@ -335,7 +342,7 @@ __global__ __launch_bounds__(1024) void pool_give_kernel(PoolParams p) {
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int r = tid * R + i;
+        const int r = i * 1024 + tid;
         if (r >= p.rows) continue;
         if constexpr (FORK) {
             if (!ok) p.plan[r] = -2;

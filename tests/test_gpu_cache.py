@@ -206,6 +206,26 @@ def test_pool(dev, rows, cols, P, spare):
         assert ds.device_error() in (0, ds.DEVERR_POOL)
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float8_e4m3fn])
+@pytest.mark.parametrize("layout", ["heads", "interleaved"])
+@pytest.mark.parametrize("P,part", [(16, 15), (16, 1), (40, 33), (64, 64)])
+def test_fork_copies_only_what_is_used(dev, dt, layout, P, part):
+    """The slots in use of the partial page, every layer and head of any layout; all else stays as it was."""
+    k, v = _caches(dev, 3, 6, P, 2, 32, layout, dt)
+    want = [_bits(k), _bits(v)]
+    t = lambda *a: torch.tensor(a, dtype=torch.int32, device=dev)
+    n = 2 * P + part
+    p = ds.Pages(torch.tensor([[-1] * 4, [4, 1, 3, -1]], dtype=torch.int32, device=dev), t(0, 3), t(0, n),
+                 t(0, 1, 0, 1, 1, 0), P)
+    assert ds.pages_fork(p, t(1, -1), k, v).tolist() == [1] and ds.device_error() == 0
+    if part < P:
+        for w in want:
+            w[:, 0, :part] = w[:, 3, :part]
+    assert p.table.tolist() == [[4, 1, 0 if part < P else 3, -1], [4, 1, 3, -1]]
+    assert p.refcount.tolist() == ([1, 2, 0, 1, 2, 0] if part < P else [0, 2, 0, 2, 2, 0]) and p.seq_len.tolist() == [n, n]
+    assert np.array_equal(_bits(k), want[0]) and np.array_equal(_bits(v), want[1])
+
+
 def test_pool_runs_short(dev):
     """Too few free pages for all rows: nothing changes, and it is said."""
     P = 4
@@ -288,6 +308,17 @@ def test_large_pools(dev):
     p = ds.Pages(t, z.clone(), z.clone(), torch.zeros(100, dtype=torch.int32, device=dev), 1)
     assert ds.pages_reserve(p, z + (1 << 29)).tolist() == [0] and ds.device_error() == ds.DEVERR_POOL
     assert (p.row_pages == 0).all() and (p.refcount == 0).all() and (t[:, :4] == -1).all()
+    # the same of a pool of more than 2^20 pages, and a wish that it just holds
+    ref = torch.zeros((1 << 20) + 5, dtype=torch.int32, device=dev)
+    p = ds.Pages(t, z.clone(), z.clone(), ref, 1)
+    assert ds.pages_reserve(p, z + (1 << 29)).tolist() == [0] and ds.device_error() == ds.DEVERR_POOL
+    want = z.clone()
+    want[3], want[5] = 1 << 20, 6
+    assert ds.pages_reserve(p, want).tolist() == [0] and ds.device_error() == ds.DEVERR_POOL and (ref == 0).all()
+    want[5] = 5
+    assert ds.pages_reserve(p, want).tolist() == [1] and ds.device_error() == 0 and (ref == 1).all()
+    assert t[5, :6].tolist() == [(1 << 20) + i for i in range(5)] + [-1] and t[3, [0, -1]].tolist() == [0, -1]
+    assert p.row_pages.tolist() == [0, 0, 0, 1 << 20, 0, 5, 0, 0]
     del t, p
     e = torch.zeros(0, dtype=torch.int32, device=dev)
     p = ds.Pages(torch.zeros((0, 2), dtype=torch.int32, device=dev), e, e, ref, 2)
