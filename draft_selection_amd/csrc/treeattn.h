@@ -32,9 +32,9 @@
 // on the vector unit beside the products); one token over 333, 8.8 and 3 (a chain
 // of loads: lengths, page ids, keys).
 //
-// Keys move from the cache into a ring of two LDS stages by 16-byte LDS-DMA
-// loads (global_load_lds_dwordx4), one round ahead; page ids one round before
-// that.  16-byte chunk c of tile row `row` lies at chunk c ^ key(row); the keys
+// Keys move from the cache into a ring of two or three LDS stages by 16-byte
+// LDS-DMA loads (global_load_lds_dwordx4), one or two rounds ahead; page ids as
+// many rounds before that.  16-byte chunk c of tile row `row` lies at chunk c ^ key(row); the keys
 // spread what one LDS pass reads over all 64 banks.
 #pragma once
 

@@ -330,6 +330,35 @@ def test_same_bits_on_every_call_and_stream(dev):
         assert torch.equal(o, first) and torch.equal(l, l1)
 
 
+def test_captured_and_replayed(dev):
+    """Two captured calls that share a workspace, one after the other, replayed between eager calls on changed inputs:
+    every replay gives what an eager call gives."""
+    rng = np.random.default_rng(12)
+    q, a, *_ = _setup(rng, dev, 3, 20, 8, 2, 128, 16, [3000, 50, 700], torch.bfloat16)
+    q2, a2, *_ = _setup(rng, dev, 2, 40, 8, 1, 64, 16, [600, 900], torch.float8_e4m3fn)
+    ws = torch.empty(max(ds.tree_attn_workspace_bytes(3, 20, 8, 2, 128, torch.bfloat16, 1 << 20),
+                         ds.tree_attn_workspace_bytes(2, 40, 8, 1, 64, torch.float8_e4m3fn, 1 << 20)),
+                     dtype=torch.uint8, device=dev)
+    ws.fill_(0xFF)
+    outs = [torch.zeros_like(q), torch.zeros_like(q2)]
+    graphs = []
+    for x, args, o in ((q, a, outs[0]), (q2, a2, outs[1])):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ds.tree_attn(x, out=o, workspace=ws, **args)
+        graphs.append(g)
+    for step in range(4):
+        q.copy_(torch.randn(q.shape, device=dev).to(torch.bfloat16))
+        q2.copy_(torch.randn(q2.shape, device=dev).to(torch.bfloat16))
+        if step:
+            a["seq_len"] -= 7                                     # a shorter cache: other shares, other joins
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ds.tree_attn(q, **a)[0], outs[0]) and torch.equal(ds.tree_attn(q2, **a2)[0], outs[1])
+    assert ds.device_error() == 0
+
+
 def test_refusals(dev):
     rng = np.random.default_rng(4)
     q, a, *_ = _setup(rng, dev, 2, 5, 4, 2, 64, 16, [30, 9], torch.bfloat16)
