@@ -1130,8 +1130,7 @@ DSEL_API dsel_status dsel_dyn_conv(const uint16_t *x, const uint16_t *x_prev, co
 namespace {
 
 // Checks a cache and lays its strides out in 16-byte vectors.  A stride of an
-// extent of one is never used and may be anything.  `data` false: only the
-// page geometry is used, and K, V may be missing.
+// extent of one is never used and may be anything.
 dsel_status check_cache(const dsel_cache *c, CacheView *v) {
     if (!c) return DSEL_E_ARG;
     if (c->dt != DSEL_BF16 && c->dt != DSEL_E4M3) return DSEL_E_DTYPE;
@@ -1241,11 +1240,11 @@ namespace {
 // a K/V head) there are, padded head dim by the head dim.
 struct AttnKernels {
     const void *attn, *join;
-    int threads, rows, wgs, part, join_y;
+    int threads, wgs, part, join_y;
 };
 template <class C>
 AttnKernels attn_kernels() {
-    return {(const void *)tree_attn_kernel<C>, (const void *)tree_attn_join_kernel<C>, C::NT, C::ROWS,
+    return {(const void *)tree_attn_kernel<C>, (const void *)tree_attn_join_kernel<C>, C::NT,
             kAttnCUs * C::WGS, C::PART, AttnJoin<C>::Y};
 }
 template <bool E4M3>

@@ -479,7 +479,9 @@ dsel_status dsel_dyn_conv(const uint16_t *x, const uint16_t *x_prev, const uint1
  * block and sets DSEL_DEVERR_SEQ_LEN.  Entries of page_table past the positions
  * in use are never read; a page id in use outside [0, num_pages) sets
  * DSEL_DEVERR_PAGE and its positions are seen by no query (attention), or not
- * written (append), or leave the whole row as it was (compact). */
+ * written (append), or leave the whole row as it was (compact).
+ *
+ * The device that is current at a call must be that of its pointers and stream. */
 #define DSEL_MAX_TREE 256          /* nodes of a tree */
 #define DSEL_MAX_TREE_BATCH 65535  /* batch rows of these calls */
 #define DSEL_MAX_HEAD_DIM 256
