@@ -1337,7 +1337,7 @@ DSEL_API dsel_status dsel_cache_append(const uint16_t *k_new, const uint16_t *v_
                                        const dsel_cache *cache, const int32_t *page_table, int64_t table_ld,
                                        int64_t max_pages, const int32_t *seq_len, int64_t batch, int64_t block,
                                        const int32_t *block_len, dsel_stream_t stream) {
-    if (batch < 0 || batch > DSEL_MAX_TREE_BATCH || block < 0 || block > INT_MAX / 2) return DSEL_E_ARG;
+    if (batch < 0 || batch > DSEL_MAX_TREE_BATCH || block < 0 || block > DSEL_MAX_APPEND) return DSEL_E_ARG;
     AppendParams p{};
     dsel_status st = check_cache(cache, &p.c);
     if (st != DSEL_OK) return st;

@@ -484,6 +484,7 @@ dsel_status dsel_dyn_conv(const uint16_t *x, const uint16_t *x_prev, const uint1
  * The device that is current at a call must be that of its pointers and stream. */
 #define DSEL_MAX_TREE 256          /* nodes of a tree */
 #define DSEL_MAX_TREE_BATCH 65535  /* batch rows of these calls */
+#define DSEL_MAX_APPEND 536870912  /* tokens of a row that dsel_cache_append takes */
 #define DSEL_MAX_HEAD_DIM 256
 #define DSEL_MAX_HEADS 1024
 #define DSEL_MAX_LAYERS 1024
@@ -597,7 +598,7 @@ dsel_status dsel_tree_accept(const int32_t *parent, const int32_t *tok, const in
  * E4M3 caches take x / scale (one fp32 rounding), held to +-448 and rounded to
  * nearest even.  seq_len is not changed.  The pages written must be held by
  * their row alone, as dsel_pages_reserve and dsel_pages_fork leave them.
- * `block` may be of any length here (a whole prompt). */
+ * `block` may be of any length up to DSEL_MAX_APPEND here (a whole prompt). */
 dsel_status dsel_cache_append(const uint16_t *k_new, const uint16_t *v_new, const int64_t strides[4],
                               const dsel_cache *cache, const int32_t *page_table, int64_t table_ld,
                               int64_t max_pages, const int32_t *seq_len, int64_t batch, int64_t block,

@@ -93,6 +93,8 @@ def test_append_and_compact_validation(lib):
     assert append(st=(0, 9 * 1024, 1020, 128)) == -3 and append(st=(0, -8, 1024, 128)) == -1 and append(k=F + 4) == -3
     assert append(table=None) == -1 and append(seq=None) == -1 and append(ld=2) == -1 and append(lens=F + 1) == -3
     assert append(B=0, k=None, v=None) == 0 and append(T=0, k=None, v=None) == 0 and append(B=65536) == -1
+    # one token past the longest block: a grid of 2^32 threads comes at twice that, and no device takes it
+    assert append(st=(0, 0, 0, 128), T=(1 << 29) + 1) == -1 and append(st=(0, 0, 0, 128), T=(1 << 30) - 1) == -1
 
     def compact(table=F, seq=F, path=F, n=F, B=2, T=9, new=F + 64):
         return lib.dsel_cache_compact(C.byref(_cache()), table, 4, 4, seq, path, n, B, T, new, None)
