@@ -739,8 +739,14 @@ def _placed(fn):
     device's current stream), both made current, so that what it allocates
     belongs to the stream its kernels are launched on."""
 
+    sig = inspect.signature(fn)
+    params = list(sig.parameters.values())
+
     @functools.wraps(fn)
-    def wrap(first, *args, stream=None, **kwargs):
+    def wrap(*args, stream=None, **kwargs):
+        first = args[0] if args else kwargs.get(params[0].name)
+        if first is None:
+            raise TypeError(f"{fn.__name__}: {params[0].name} is missing")
         t = first.table if isinstance(first, Pages) else first
         if not t.is_cuda:
             raise ValueError(f"{fn.__name__}: the tensors must be on the GPU")
@@ -748,12 +754,14 @@ def _placed(fn):
             if stream.device != t.device:
                 raise ValueError(f"{fn.__name__}: stream is of {stream.device}, the tensors are on {t.device}")
             with torch.cuda.stream(stream):
-                return fn(first, *args, **kwargs)
+                return fn(*args, **kwargs)
         if t.get_device() != torch.cuda.current_device():
             with torch.cuda.device(t.device):
-                return fn(first, *args, **kwargs)
-        return fn(first, *args, **kwargs)
+                return fn(*args, **kwargs)
+        return fn(*args, **kwargs)
 
+    wrap.__signature__ = sig.replace(parameters=[*params, inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY,
+                                                                            default=None)])
     return wrap
 
 

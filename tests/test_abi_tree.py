@@ -2,8 +2,10 @@
 
 CPU only: every call below fails validation or has nothing to do."""
 import ctypes as C
+import inspect
 
 import pytest
+import torch
 
 import draft_selection_amd as ds
 
@@ -138,3 +140,20 @@ def test_binding_refuses_host_tensors():
                     (ds.pages_free, (ds.Pages(z, z[:, 0], z[:, 0], z[0], 16), z[:, 0]))):
         with pytest.raises(ValueError):
             f(*args)
+
+
+def test_calls_take_their_arguments_by_name():
+    """The first argument, whose device a call runs on, may be given by name as any other; a missing one is named."""
+    x = torch.zeros(2, 3, dtype=torch.int32)
+    pages = ds.Pages(x, x[:, 0], x[:, 0], x[0], 16)
+    for fn, kw in [(ds.tree_mask, dict(parent=x)), (ds.tree_accept, dict(parent=x, tok=x, target_tok=x)),
+                   (ds.tree_attn, dict(q=x, k_cache=x, v_cache=x, page_table=x, seq_len=x)),
+                   (ds.cache_append, dict(k_new=x, v_new=x, k_cache=x, v_cache=x, page_table=x, seq_len=x)),
+                   (ds.cache_compact, dict(k_cache=x, v_cache=x, page_table=x, seq_len=x, path=x, n_keep=x)),
+                   (ds.pages_reserve, dict(pages=pages, extra=x)), (ds.pages_free, dict(pages=pages, which=x)),
+                   (ds.pages_fork, dict(pages=pages, src=x, k_cache=x, v_cache=x))]:
+        with pytest.raises(ValueError, match="on the GPU"):
+            fn(**kw)
+        with pytest.raises(TypeError, match="missing"):
+            fn()
+        assert list(inspect.signature(fn).parameters)[-1] == "stream"

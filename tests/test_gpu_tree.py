@@ -106,3 +106,15 @@ def test_empty_batch_and_refusals(dev):
         ds.tree_accept(p, p, torch.zeros((2, 10), dtype=torch.int32, device=dev)[:, :5])  # rows not evenly spaced
     with pytest.raises(ValueError):
         ds.tree_mask(p, block_len=torch.zeros(3, dtype=torch.int32, device=dev))
+
+
+def test_arguments_by_name_and_on_a_stream(dev):
+    rng = np.random.default_rng(9)
+    parent, tok, target = (torch.from_numpy(x).to(dev) for x in _case(rng, 3, 40, "random"))
+    want = ds.tree_mask(parent), ds.tree_accept(parent, tok, target)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = ds.tree_mask(parent=parent, stream=s), ds.tree_accept(target_tok=target, tok=tok, parent=parent, stream=s)
+    s.synchronize()
+    for x, y in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(x, y))
