@@ -376,8 +376,10 @@ __device__ __forceinline__ void attn_mask(AttnScores<C> &s, uint64_t see) {
     }
 }
 
-// The running maximum only moves (and the sums are only scaled) when a row's
-// scores pass it by more than 8: weights stay below 2^8, as exact as any others.
+// The running maximum of a row only moves (and its sums are only scaled) when
+// the row's own scores pass it by more than 8: weights stay below 2^8, as exact
+// as any others.  The other rows of the wave are scaled by 1 then, so that when
+// they move, and with it every rounding, depends on no row but their own.
 template <class C>
 __device__ __forceinline__ void attn_rescale(AttnState<C> &a, const AttnScores<C> &s, float c) {
     float top = -__builtin_inff();
@@ -386,15 +388,15 @@ __device__ __forceinline__ void attn_rescale(AttnState<C> &a, const AttnScores<C
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[sub][i]);
     top = fmaxf(top, __uint_as_float(xor_lane32<32>(__float_as_uint(top)))) * c;
-    if (ballot(top > a.m + 8.0f)) {
-        const float m = fmaxf(a.m, top);
-        const float f = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(a.m - m);
+    const bool move = top > a.m + 8.0f;
+    if (ballot(move)) {
+        const float f = move ? __builtin_amdgcn_exp2f(a.m - top) : 1.0f;
 #pragma unroll
         for (int nb = 0; nb < C::NB; ++nb)
 #pragma unroll
             for (int i = 0; i < 16; ++i) a.o[nb][i] *= f;
         a.l *= f;
-        a.m = m;
+        if (move) a.m = top;
     }
 }
 

@@ -1,0 +1,34 @@
+"""tree_attn on the GPU: what a node's result may depend on, down to its bits."""
+import numpy as np
+import pytest
+import torch
+
+import draft_selection_amd as ds
+import test_gpu_tree_attn as ta
+
+pytestmark = pytest.mark.gpu
+DTYPES = ta.DTYPES
+
+
+def _bits(o, l):
+    return o.view(torch.int16).clone(), l.view(torch.int32).clone()
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("T,Hq,H,D", [(5, 4, 2, 64), (9, 4, 1, 128), (17, 4, 1, 128), (40, 8, 1, 128), (6, 8, 1, 256),
+                                      (21, 8, 1, 256)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_other_queries_change_no_bit(dev, dt, T, Hq, H, D, wide):
+    """The queries of other nodes and other heads, whose running maximum moves at other keys, leave a result as it is."""
+    rng = np.random.default_rng(T * D)
+    q, a, *_ = ta._setup(rng, dev, 2, T, Hq, H, D, 16, [230, 180] if not wide else [3000, 900], dt)
+    if wide:
+        a = ta._widen(a)
+    first = _bits(*ds.tree_attn(q, want_lse=True, **a))
+    keep = torch.zeros(q.shape[:3], dtype=torch.bool, device=dev)
+    keep[:, ::3, 1] = True                                        # these queries stay, every other one grows
+    for factor in (8.0, 60.0, 0.0):
+        p = torch.where(keep[..., None], q, (factor * q.float()).to(torch.bfloat16))
+        got = _bits(*ds.tree_attn(p, want_lse=True, **a))
+        assert torch.equal(got[0][keep], first[0][keep]) and torch.equal(got[1][keep], first[1][keep])
+    assert ds.device_error() == 0
