@@ -501,12 +501,18 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
         const char *const vbase = p.c.v + 16 * (hk * p.c.head_stride);
         const int32_t *const table = p.t.table + b * p.t.ld;
         float c = p.scale;
-        bool flip = false;  // a negative scale changes q's sign, so that c stays positive
+        // c is a positive number, so that a masked score of -inf stays one times c:
+        // what a scale's sign or NaN does to the scores is done to q
+        uint32_t sign = 0, nan = 0;
         if (C::E4M3 && p.c.k_scale) {
             const float ks = p.c.k_scale[hk];
-            flip = ks < 0.0f;
+            sign = ks < 0.0f ? 0x80008000u : 0u;
             c = p.scale * fabsf(ks);
-            if (c == 0.0f) c = 1e-37f;  // (a score of -inf stays one)
+            if (c == 0.0f) c = 1e-37f;
+            if (c != c) {
+                nan = 0x7FC07FC0u;
+                c = 1.0f;
+            }
         }
 
         // the lane's rows, and their q: eight values of every 16-deep step
@@ -520,7 +526,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
         for (int ks = 0; ks < C::DP / 16; ++ks) {
             const int d = C::E4M3 ? 32 * (ks >> 1) + 16 * h + 8 * (ks & 1) : 16 * ks + 8 * h;
             u32x4 w = live && d < p.D ? *(const u32x4 *)(qr + d) : u32x4{0, 0, 0, 0};
-            if (C::E4M3 && flip) w ^= 0x80008000u;
+            if constexpr (C::E4M3) w = (w ^ sign) | nan;
             q[ks] = __builtin_bit_cast(bf16x8, w);
         }
 
