@@ -1130,8 +1130,9 @@ DSEL_API dsel_status dsel_dyn_conv(const uint16_t *x, const uint16_t *x_prev, co
 namespace {
 
 // Checks a cache and lays its strides out in 16-byte vectors.  A stride of an
-// extent of one is never used and may be anything.
-dsel_status check_cache(const dsel_cache *c, CacheView *v) {
+// extent of one is never used and may be anything; so may the pointers of a call
+// with no work.
+dsel_status check_cache(const dsel_cache *c, bool work, CacheView *v) {
     if (!c) return DSEL_E_ARG;
     if (c->dt != DSEL_BF16 && c->dt != DSEL_E4M3) return DSEL_E_DTYPE;
     const int64_t es = c->dt == DSEL_BF16 ? 2 : 1, per = 16 / es;
@@ -1139,9 +1140,10 @@ dsel_status check_cache(const dsel_cache *c, CacheView *v) {
         c->dim > DSEL_MAX_HEAD_DIM || c->num_pages < 1 || c->num_pages > INT_MAX || c->page_size < 1 ||
         c->page_size > DSEL_MAX_PAGE)
         return DSEL_E_ARG;
-    if (!c->k || !c->v) return DSEL_E_ARG;
+    if (work && (!c->k || !c->v)) return DSEL_E_ARG;
     if (c->dt == DSEL_BF16 && (c->k_scale || c->v_scale)) return DSEL_E_ARG;
-    if (c->dim % per || !aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+    if (c->dim % per) return DSEL_E_ALIGN;
+    if (work && (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)))
         return DSEL_E_ALIGN;
     const int64_t extent[4] = {c->layers, c->num_pages, c->page_size, c->heads};
     const int64_t stride[4] = {c->layer_stride, c->page_stride, c->slot_stride, c->head_stride};
@@ -1283,7 +1285,7 @@ DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cac
     dsel_status st = check_tree(a->batch, a->block);
     if (st != DSEL_OK) return st;
     TreeAttnParams p{};
-    if ((st = check_cache(cache, &p.c)) != DSEL_OK) return st;
+    if ((st = check_cache(cache, a->batch > 0, &p.c)) != DSEL_OK) return st;
     if (cache->layers != 1 || a->q_heads < 1 || a->q_heads > DSEL_MAX_HEADS || a->q_heads % cache->heads)
         return DSEL_E_ARG;
     if (!(a->scale > 0.0f && a->scale < __builtin_inff())) return DSEL_E_ARG;
@@ -1339,7 +1341,7 @@ DSEL_API dsel_status dsel_cache_append(const uint16_t *k_new, const uint16_t *v_
                                        const int32_t *block_len, dsel_stream_t stream) {
     if (batch < 0 || batch > DSEL_MAX_TREE_BATCH || block < 0 || block > DSEL_MAX_APPEND) return DSEL_E_ARG;
     AppendParams p{};
-    dsel_status st = check_cache(cache, &p.c);
+    dsel_status st = check_cache(cache, batch > 0 && block > 0, &p.c);
     if (st != DSEL_OK) return st;
     if ((st = check_table(page_table, table_ld, max_pages, cache->page_size, seq_len, batch, block, block_len, &p.t)) !=
         DSEL_OK)
@@ -1377,7 +1379,7 @@ DSEL_API dsel_status dsel_cache_compact(const dsel_cache *cache, const int32_t *
     dsel_status st = check_tree(batch, block);
     if (st != DSEL_OK) return st;
     CompactParams p{};
-    if ((st = check_cache(cache, &p.c)) != DSEL_OK) return st;
+    if ((st = check_cache(cache, batch > 0, &p.c)) != DSEL_OK) return st;
     if ((st = check_table(page_table, table_ld, max_pages, cache->page_size, seq_len, batch, block, nullptr, &p.t)) !=
         DSEL_OK)
         return st;
@@ -1442,7 +1444,7 @@ DSEL_API dsel_status dsel_pages_fork(const dsel_pages *pages, const int32_t *src
     CacheView c{};
     dsel_status st = check_pages(pages, src, &p);
     if (st != DSEL_OK) return st;
-    if ((st = check_cache(cache, &c)) != DSEL_OK) return st;
+    if ((st = check_cache(cache, pages->rows > 0, &c)) != DSEL_OK) return st;
     if (cache->num_pages != pages->num_pages || cache->page_size != pages->page_size) return DSEL_E_ARG;
     if (pages->rows == 0) return DSEL_OK;
     if (!granted) return DSEL_E_ARG;

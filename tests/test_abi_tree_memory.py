@@ -1,0 +1,30 @@
+"""Host-side validation of the tree and cache calls: which memory they take.
+
+CPU only: every call below has nothing to do or fails validation."""
+import ctypes as C
+
+import pytest
+
+import draft_selection_amd as ds
+import test_abi_tree as at
+
+F = at.F
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return ds.lib()
+
+
+def test_nothing_to_do_needs_no_memory(lib):
+    """With no work every pointer may be NULL, those of the cache among them; its sizes are still checked."""
+    for bad, code in ((dict(), 0), (dict(heads=0), -1), (dict(dim=100), -3), (dict(dt=0), -2), (dict(slot_stride=-8), -1)):
+        c = at._cache(k=None, v=None, **bad)
+        none = dict(q=None, out=None, page_table=None, seq_len=None, ws=None, wsb=0)
+        assert at._attn(lib, c, batch=0, **none) == code
+        for B, T in ((0, 9), (2, 0)):
+            assert lib.dsel_cache_append(None, None, None, C.byref(c), None, 4, 4, None, B, T, None, None) == code
+        assert lib.dsel_cache_compact(C.byref(c), None, 4, 4, None, None, None, 0, 9, None, None) == code
+        p = ds.PagesArgs(None, 4, 0, 4, None, None, None, 10, 16)
+        assert lib.dsel_pages_fork(C.byref(p), None, C.byref(c), None, None, 0, None) == code
+    assert at._attn(lib, at._cache(k=None)) == -1 and at._attn(lib, at._cache(v=None)) == -1
