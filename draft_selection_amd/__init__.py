@@ -971,7 +971,8 @@ def cache_append(k_new, v_new, k_cache, v_cache, page_table, seq_len, block_len=
 def cache_compact(k_cache, v_cache, page_table, seq_len, path, n_keep, new_len=None):
     """Keeps a path of the appended tokens: in every layer the rows at ``seq_len[b]
     + path[b, i]`` move to ``seq_len[b] + i`` for ``i < n_keep[b]`` (path ascends, as
-    tree_accept gives it).  Returns ``new_len [B]`` int32, the rows' new lengths."""
+    tree_accept gives it).  Returns ``new_len [B]`` int32, the rows' new lengths (a
+    given ``new_len`` shares no memory with the other arguments)."""
     dev = k_cache.device
     cache, _ = _cache(dev, k_cache, v_cache)
     B, T = path.shape

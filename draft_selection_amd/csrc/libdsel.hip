@@ -30,6 +30,11 @@ using namespace dsel;
 
 inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+// Do the na bytes from a on and the nb bytes from b on share any?
+inline bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+    return (uintptr_t)a < (uintptr_t)b + (uintptr_t)nb && (uintptr_t)b < (uintptr_t)a + (uintptr_t)na;
+}
+
 inline dsel_status launch(const void *kernel, dim3 grid, dim3 block, void *arg, size_t shmem,
                           dsel_stream_t stream) {
     void *args[] = {arg};
@@ -1384,8 +1389,13 @@ DSEL_API dsel_status dsel_cache_compact(const dsel_cache *cache, const int32_t *
         DSEL_OK)
         return st;
     if (batch == 0) return DSEL_OK;
-    if (!path || !n_keep || !new_len || new_len == seq_len) return DSEL_E_ARG;
+    if (!path || !n_keep || !new_len) return DSEL_E_ARG;
     if (!aligned(path, 4) || !aligned(n_keep, 4) || !aligned(new_len, 4)) return DSEL_E_ALIGN;
+    // a row's first workgroup writes new_len while its others still read these
+    const int64_t nb = batch * (int64_t)sizeof(int32_t);
+    if (overlap(new_len, nb, seq_len, nb) || overlap(new_len, nb, n_keep, nb) || overlap(new_len, nb, path, nb * block) ||
+        overlap(new_len, nb, page_table, ((batch - 1) * table_ld + max_pages) * (int64_t)sizeof(int32_t)))
+        return DSEL_E_ARG;
     p.path = path;
     p.n_keep = n_keep;
     p.new_len = new_len;

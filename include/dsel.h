@@ -610,7 +610,7 @@ dsel_status dsel_cache_append(const uint16_t *k_new, const uint16_t *v_new, cons
  *            below block; n_keep [batch] int32, 0 <= n_keep[b] <= block.  Other
  *            values set DSEL_DEVERR_TREE and leave the row as it was.
  *   new_len  out [batch] int32: seq_len[b] + n_keep[b] (seq_len[b] for a row
- *            left as it was); must not be seq_len itself. */
+ *            left as it was); shares no memory with the inputs (DSEL_E_ARG). */
 dsel_status dsel_cache_compact(const dsel_cache *cache, const int32_t *page_table, int64_t table_ld,
                                int64_t max_pages, const int32_t *seq_len, const int32_t *path,
                                const int32_t *n_keep, int64_t batch, int64_t block, int32_t *new_len,

@@ -28,3 +28,15 @@ def test_nothing_to_do_needs_no_memory(lib):
         p = ds.PagesArgs(None, 4, 0, 4, None, None, None, 10, 16)
         assert lib.dsel_pages_fork(C.byref(p), None, C.byref(c), None, None, 0, None) == code
     assert at._attn(lib, at._cache(k=None)) == -1 and at._attn(lib, at._cache(v=None)) == -1
+
+
+def test_compact_writes_lengths_apart_from_what_it_reads(lib):
+    """Workgroups of a row read its length, path and table while one of them writes new_len: no byte may be shared."""
+    far = 1 << 20
+    seq, path, n, table = F, F + far, F + 2 * far, F + 3 * far    # [5], [5, 9], [5], 5 rows of 4, 6 apart
+
+    def compact(new):
+        return lib.dsel_cache_compact(C.byref(at._cache()), table, 6, 4, seq, path, n, 5, 9, new, None)
+    for start, words in ((seq, 5), (n, 5), (path, 5 * 9), (table, 4 * 6 + 4)):
+        for w in (-4, 0, words - 1):
+            assert compact(start + 4 * w) == -1, (start, w)
