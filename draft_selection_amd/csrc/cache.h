@@ -136,6 +136,7 @@ struct CompactParams {
     const int32_t *path, *n_keep;
     int32_t *new_len;
     int T;
+    int kinds;  // 2: K and V; 1: one array is both, and moves once
 };
 
 // Rows s + path[i] move to s + i.  path ascends, so path[i] >= i and a row
@@ -177,9 +178,9 @@ __global__ __launch_bounds__(256) void cache_compact_kernel(CompactParams p) {
     const uint32_t vecs = p.c.vecs, cols = vecs * p.c.heads;
     const uint32_t i = blockIdx.x * 256 + tid;
     const uint32_t lk = i / cols;
-    if (lk >= 2u * p.c.layers) return;
-    const uint32_t col = i - lk * cols, h = col / vecs;
-    u32x4 *x = (u32x4 *)(lk & 1 ? p.c.v : p.c.k) + (lk >> 1) * p.c.layer_stride + h * p.c.head_stride + (col - h * vecs);
+    if (lk >= (uint32_t)(p.kinds * p.c.layers)) return;
+    const uint32_t col = i - lk * cols, h = col / vecs, both = p.kinds - 1;
+    u32x4 *x = (u32x4 *)(lk & both ? p.c.v : p.c.k) + (lk >> both) * p.c.layer_stride + h * p.c.head_stride + (col - h * vecs);
     for (int k = 0; k < n; k += 8) {
         u32x4 w[8];
 #pragma unroll

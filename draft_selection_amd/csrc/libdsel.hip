@@ -1177,6 +1177,13 @@ dsel_status check_cache(const dsel_cache *c, bool work, CacheView *v) {
     return DSEL_OK;
 }
 
+// K and V of a cache that is written, whose K and V go to different workgroups:
+// two arrays, or one as both (`tied`) whose rows are then the same for both.
+dsel_status check_kv(const dsel_cache *c, bool tied) {
+    const int64_t row = c->dim * (c->dt == DSEL_BF16 ? 2 : 1);
+    return overlap(c->k, row, c->v, row) && !(tied && c->k == c->v) ? DSEL_E_ARG : DSEL_OK;
+}
+
 // The batch that reads or writes a cache through its page table
 dsel_status check_table(const int32_t *table, int64_t ld, int64_t max_pages, int64_t page_size,
                         const int32_t *seq_len, int64_t batch, int64_t block, const int32_t *block_len,
@@ -1371,6 +1378,7 @@ DSEL_API dsel_status dsel_cache_append(const uint16_t *k_new, const uint16_t *v_
     p.sh = sn[3];
     p.T = (int)block;
     p.len = block_len;
+    if ((st = check_kv(cache, k_new == v_new && cache->k_scale == cache->v_scale)) != DSEL_OK) return st;
     const void *k = cache->dt == DSEL_E4M3 ? (const void *)cache_append_kernel<true>
                                            : (const void *)cache_append_kernel<false>;
     return launch(k, dim3((unsigned)((block + kAppendTokens - 1) / kAppendTokens), (unsigned)cache->layers * 2,
@@ -1396,11 +1404,13 @@ DSEL_API dsel_status dsel_cache_compact(const dsel_cache *cache, const int32_t *
     if (overlap(new_len, nb, seq_len, nb) || overlap(new_len, nb, n_keep, nb) || overlap(new_len, nb, path, nb * block) ||
         overlap(new_len, nb, page_table, ((batch - 1) * table_ld + max_pages) * (int64_t)sizeof(int32_t)))
         return DSEL_E_ARG;
+    if ((st = check_kv(cache, true)) != DSEL_OK) return st;
+    p.kinds = cache->k == cache->v ? 1 : 2;
     p.path = path;
     p.n_keep = n_keep;
     p.new_len = new_len;
     p.T = (int)block;
-    const int64_t vecs = 2 * (int64_t)p.c.layers * p.c.heads * p.c.vecs;
+    const int64_t vecs = (int64_t)p.kinds * p.c.layers * p.c.heads * p.c.vecs;
     return launch((const void *)cache_compact_kernel, dim3((unsigned)((vecs + 255) / 256), (unsigned)batch), dim3(256),
                   &p, 0, stream);
 }
@@ -1461,6 +1471,7 @@ DSEL_API dsel_status dsel_pages_fork(const dsel_pages *pages, const int32_t *src
     if (!aligned(granted, 4)) return DSEL_E_ALIGN;
     if (!workspace || workspace_bytes < dsel_pages_fork_workspace_bytes(pages->rows)) return DSEL_E_WORKSPACE;
     if (!aligned(workspace, 4)) return DSEL_E_ALIGN;
+    if ((st = check_kv(cache, true)) != DSEL_OK) return st;
     p.granted = granted;
     p.plan = (int32_t *)workspace;
     st = launch((const void *)pool_give_kernel<true>, dim3(1), dim3(1024), &p, 0, stream);

@@ -499,7 +499,9 @@ dsel_status dsel_dyn_conv(const uint16_t *x, const uint16_t *x_prev, const uint1
  * element stands for its 8-bit value times the scale.
  * Requirements: k, v 16-byte aligned; dim and every stride of an extent above
  * one a multiple of 16 bytes; those strides >= dim; elements of different
- * (layer, page, slot, head) distinct; 1 <= dim <= DSEL_MAX_HEAD_DIM,
+ * (layer, page, slot, head) distinct, and K and V apart or one and the same (k ==
+ * v, which dsel_cache_append takes if the new rows and scales are the same too);
+ * 1 <= dim <= DSEL_MAX_HEAD_DIM,
  * heads <= DSEL_MAX_HEADS, layers <= DSEL_MAX_LAYERS, page_size <=
  * DSEL_MAX_PAGE, max_pages * page_size < 2^31 - DSEL_MAX_PAGE. */
 typedef struct {
