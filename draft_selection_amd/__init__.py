@@ -873,7 +873,9 @@ def tree_attn(q, k_cache, v_cache, page_table, seq_len, mask=None, block_len=Non
     ``seq_len`` cached positions, and the tokens whose bits are set in its row of
     ``mask`` (tree_mask's layout; None: those up to itself).  ``scale`` defaults
     to ``dim ** -0.5``.  Returns ``(out [B, T, q_heads, dim] bf16, lse [B, T,
-    q_heads] fp32 or None)``; a token that sees nothing gets 0 and -inf."""
+    q_heads] fp32 or None)``; a token that sees nothing gets 0 and -inf.  Calls of
+    the same sizes and lengths give the same bits; a row's last bits may differ
+    from those that it gets alone or beside rows of other lengths."""
     shape, sq, dev = q.shape, q.stride(), q.device
     if len(shape) != 4 or q.dtype is not _BF16:
         raise TypeError("q must be bfloat16 [B, T, q_heads, dim]")

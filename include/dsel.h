@@ -39,7 +39,7 @@
  * array [batch] of int32 (4-byte aligned) giving block b's valid positions,
  * 0 <= block_len[b] <= block, in the same padded [batch, block] layout.  Block
  * b is then computed exactly as it would be alone at length block_len[b]
- * (same bits).  Outputs at padding positions (t >= block_len[b]) are not
+ * (same bits; dsel_tree_attn alone promises less, see there).  Outputs at padding positions (t >= block_len[b]) are not
  * written, except where a call says so, and inputs there never affect a result
  * (they may hold anything, NaN included); a length outside [0, block] makes the
  * block empty and sets DSEL_DEVERR_BLOCK_LEN.  The launch geometry is that of
@@ -542,6 +542,16 @@ dsel_status dsel_tree_mask(const int32_t *parent, int64_t batch, int64_t block, 
  * out = 0 and lse = -inf.  What a node does not see never affects its result,
  * infinities and NaN among it.  Rows of nodes past block_len[b] are not
  * written.
+ * Repeatability: calls of the same sizes (batch, block, heads, dim, max_pages *
+ * page_size) and lengths (seq_len, block_len) give the same bits, and what a node
+ * gets depends on the contents of its own query and of the keys that it sees
+ * alone, not on other queries, nodes, rows, or where pages lie.  But the work is
+ * shared out evenly over the whole batch, and a row's keys are divided, and its
+ * sums taken, accordingly: other lengths of other rows, another block or a table
+ * that holds another number of positions may change a row's last bits, within
+ * the rounding that the arithmetic below has in any order.  So a row need not
+ * get the bits that it gets alone.  It does, at the same block, where
+ * dsel_tree_attn_workspace_bytes() is 0: no row is divided then.
  * Arithmetic: the products of q and K are exact bf16 products summed in fp32
  * (E4M3 values are exact in bf16, the scales are applied to the fp32 sums); the
  * softmax's maximum, weights and sum are fp32; the weights are rounded to bf16

@@ -50,3 +50,72 @@ def test_a_scale_that_is_nan(dev, T, G, D, wide):
     assert blind.any() and not blind.all()
     assert (out[:, :, G:][blind] == 0).all() and lse[:, :, G:][blind].isneginf().all()
     assert out[:, :, G:][~blind].isnan().all() and lse[:, :, G:][~blind].isnan().all()
+
+
+SHAPES = [(1, 4, 1, 128), (7, 4, 2, 64), (17, 4, 1, 128), (40, 8, 1, 80), (21, 8, 1, 256)]
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("T,Hq,H,D", SHAPES)
+@pytest.mark.parametrize("wide", [False, True])
+def test_other_contents_change_no_bit(dev, dt, T, Hq, H, D, wide):
+    """Other rows' queries, keys and masks, the nodes that a node does not see, and where the pages lie: with the same
+    lengths none of them changes a result."""
+    rng = np.random.default_rng(T + D)
+    B, P, it = 3, 16, torch.int16 if dt == torch.bfloat16 else torch.uint8
+    q, a, _, _, vis, seq, n = ta._setup(rng, dev, B, T, Hq, H, D, P, [2000, 77, 900] if wide else [190, 77, 0], dt,
+                                        lens=[T, max(1, T - 2), T], kind="random")
+    if wide:
+        a = ta._widen(a)
+    first = _bits(*ds.tree_attn(q, want_lse=True, **a))
+    tab = a["page_table"].cpu().numpy()
+    k, v = a["k_cache"].view(it), a["v_cache"].view(it)
+    for row in range(B):
+        # every other row: new queries, new keys of ordinary size, no mask bit as it was
+        p, b = q.clone(), dict(a)
+        kk, vv = k.clone(), v.clone()
+        for r in range(B):
+            if r != row:
+                p[r] = (5 * torch.randn(q[r].shape, device=dev)).to(torch.bfloat16)
+                ids = torch.from_numpy(tab[r, :(seq[r] + n[r] + P - 1) // P].astype(np.int64)).to(dev)
+                kk[ids], vv[ids] = (torch.randn(kk[ids].shape, device=dev).to(dt).view(it) for _ in range(2))
+        b["mask"] = ~a["mask"]
+        b["mask"][row] = a["mask"][row]
+        # and in the row itself, the nodes that node t does not see
+        t = int(rng.integers(n[row]))
+        for j in np.nonzero(~vis[row, t, :n[row]])[0]:
+            at = tab[row, (seq[row] + j) // P], (seq[row] + j) % P
+            kk[at], vv[at] = (torch.randn(kk[at].shape, device=dev).to(dt).view(it) for _ in range(2))
+        # the pages in another order
+        order = torch.from_numpy(rng.permutation(len(kk))).to(dev)
+        b["k_cache"], b["v_cache"] = torch.empty_like(kk), torch.empty_like(vv)
+        b["k_cache"][order], b["v_cache"][order] = kk, vv
+        b["k_cache"], b["v_cache"] = b["k_cache"].view(dt), b["v_cache"].view(dt)
+        inside = (a["page_table"] >= 0) & (a["page_table"] < len(kk))
+        b["page_table"] = torch.where(inside, order[a["page_table"].clamp(0, len(kk) - 1).long()].int(), a["page_table"])
+        got = _bits(*ds.tree_attn(p, want_lse=True, **b))
+        assert torch.equal(got[0][row, t], first[0][row, t]) and torch.equal(got[1][row, t], first[1][row, t])
+    assert ds.device_error() == 0
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("T,Hq,H,D", SHAPES)
+def test_a_row_alone(dev, dt, T, Hq, H, D):
+    """Undivided rows get the bits that they get alone at the same block; divided ones the same to rounding."""
+    rng = np.random.default_rng(T * 3 + D)
+    for ctx, whole in (([200, 9, 0, 120], True), ([3000, 9, 0, 700], False)):
+        ctx = [min(c, 240 - T) for c in ctx] if whole else ctx
+        q, a, *ref = ta._setup(rng, dev, 4, T, Hq, H, D, 16, ctx, dt, lens=[T, 1, T, T - T // 3], spare_cols=0)
+        n = ref[4]
+        cap = a["page_table"].shape[1] * 16
+        assert (ds.tree_attn_workspace_bytes(4, T, Hq, H, D, dt, cap) == 0) == whole
+        out, lse = ds.tree_attn(q, want_lse=True, **a)
+        ta._check(out, lse, q, *ref, D ** -0.5)
+        for b in range(4):
+            one = {**a, **{k: a[k][b:b + 1] for k in ("page_table", "seq_len", "mask", "block_len")}}
+            o, l = ds.tree_attn(q[b:b + 1], want_lse=True, **one)
+            K, V, vis, seq, _ = (r[b:b + 1] for r in ref)
+            ta._check(o, l, q[b:b + 1], K, V, vis, seq, n[b:b + 1], D ** -0.5)
+            if whole:
+                assert torch.equal(o[0, :n[b]], out[b, :n[b]]) and torch.equal(l[0, :n[b]], lse[b, :n[b]])
+        assert ds.device_error() == 0
