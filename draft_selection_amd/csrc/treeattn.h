@@ -268,7 +268,11 @@ __device__ __forceinline__ bf16x8 v_operand(const char *vt, int sub, int kk, int
 // do not see every key is looked through for them; if it holds any they are
 // taken out of the products and counted apart, among the keys that each row
 // sees: +inf as 1, -inf as 32, NaN as 1024 (below 32 of each per product, so
-// the sum tells them apart).
+// the sum tells them apart).  Counted so, an infinity that a row sees is one
+// whatever its weight; in a tile that every row sees whole, which is not looked
+// through, the product makes it NaN if its weight is 0.  Either way the element
+// is not finite, which is all that is promised: looking through every tile would
+// read V twice.
 template <class C>
 __device__ __forceinline__ bool tile_special(const char *vt) {
     bool r = false;

@@ -539,9 +539,13 @@ dsel_status dsel_tree_mask(const int32_t *parent, int64_t batch, int64_t block, 
  *   out    [batch, block, q_heads, dim] bf16, rounded once to nearest even.
  *   lse    [batch, block, q_heads] fp32 (nullable).
  * A node that sees nothing (no cached position and an empty mask row) gets
- * out = 0 and lse = -inf.  What a node does not see never affects its result,
- * infinities and NaN among it.  Rows of nodes past block_len[b] are not
- * written.
+ * out = 0 and lse = -inf; so does one whose scores are all -inf.  What a node does
+ * not see never affects its result, infinities and NaN among it.  Of what it
+ * sees, a NaN score (or one of +inf) makes its whole row NaN, a NaN in V that
+ * element of out, and an infinity in V makes that element infinite or NaN, which
+ * of the two depending on where the key lies (0 times infinity is NaN, and
+ * weights below 2^-126 may be 0 or not).  Rows of nodes past block_len[b] are
+ * not written.
  * Repeatability: calls of the same sizes (batch, block, heads, dim, max_pages *
  * page_size) and lengths (seq_len, block_len) give the same bits, and what a node
  * gets depends on the contents of its own query and of the keys that it sees

@@ -119,3 +119,88 @@ def test_a_row_alone(dev, dt, T, Hq, H, D):
             if whole:
                 assert torch.equal(o[0, :n[b]], out[b, :n[b]]) and torch.equal(l[0, :n[b]], lse[b, :n[b]])
         assert ds.device_error() == 0
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("T,Hq,H,D", SHAPES)
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("q_std", [0.0, 2.0, 200.0])
+def test_infinities_and_nan_that_are_seen(dev, dt, T, Hq, H, D, wide, q_std):
+    """In cached positions, whose weights are of every size, 0 among them, and among the nodes: a NaN in V makes its
+    element NaN, an infinity makes it infinite or NaN, and the other elements stay what they are."""
+    rng = np.random.default_rng(T + D)
+    q, a, K, V, vis, seq, n = ta._setup(rng, dev, 2, T, Hq, H, D, 16, [2000, 300] if wide else [200, 0], dt, kind="all",
+                                        q_std=q_std)
+    if wide:
+        a = ta._widen(a)
+    tab = a["page_table"].cpu().numpy()
+    inf = float("inf") if dt == torch.bfloat16 else float("nan")
+    plain = torch.arange(D, device=dev) % 4 == 3
+    for b in range(2):
+        for p in {5 % (seq[b] + T), seq[b] // 2, seq[b] + T // 2}:
+            at = int(tab[b, p // 16]), p % 16
+            x = a["v_cache"][at].float()
+            x[:, 0::4], x[:, 1::4], x[:, 2::4] = inf, -inf, float("nan")
+            a["v_cache"][at] = x.to(dt)
+    out, lse = ds.tree_attn(q, want_lse=True, **a)
+    assert out[..., 2::4].isnan().all() and not out[..., 0::4].isfinite().any() and not out[..., 1::4].isfinite().any()
+    if dt == torch.bfloat16:
+        assert not (out[..., 0::4] == -inf).any() and not (out[..., 1::4] == inf).any()
+    cols = np.arange(D) % 4 == 3
+    keep = lambda x: np.where(cols, x, 0.0)
+    ta._check(torch.where(plain, out, 0), lse, q, K, [keep(v) for v in V], vis, seq, n, D ** -0.5)
+    assert ds.device_error() == 0
+
+
+@pytest.mark.parametrize("T,Hq,H,D", SHAPES)
+@pytest.mark.parametrize("wide", [False, True])
+def test_scores_of_minus_infinity(dev, T, Hq, H, D, wide):
+    """Keys whose scores are -inf have no weight; a node that sees only such gets 0 and -inf, whatever their V."""
+    rng = np.random.default_rng(T)
+    q, a, K, V, vis, seq, n = ta._setup(rng, dev, 2, T, Hq, H, D, 16, [700, 900] if wide else [130, 150], torch.bfloat16,
+                                        kind="chain")
+    if wide:
+        a = ta._widen(a)
+    q[..., 0] = q[..., 0].abs() + 1
+    tab = a["page_table"].cpu().numpy()
+
+    def put(b, p):
+        a["k_cache"][int(tab[b, p // 16]), p % 16, :, 0] = -float("inf")
+    gone = np.sort(rng.permutation(seq[1] + T)[:(seq[1] + T) // 2])
+    for p in range(seq[0] + T):
+        put(0, p)
+    for p in gone:
+        put(1, int(p))
+    a["v_cache"][int(tab[0, 0]), 3] = float("inf")
+    a["v_cache"][int(tab[0, (seq[0] + T - 1) // 16]), (seq[0] + T - 1) % 16] = float("nan")
+    out, lse = ds.tree_attn(q, want_lse=True, **a)
+    assert (out[0] == 0).all() and lse[0].isneginf().all()
+    left = np.ones(seq[1] + T, bool)
+    left[gone] = False
+    for t in range(T):
+        m = left.copy()
+        m[seq[1] + t + 1:] = False
+        if m.any():
+            ta._check(out[1:, t:t + 1], lse[1:, t:t + 1], q[1:, t:t + 1], [K[1][m]], [V[1][m]], np.ones((1, 1, 1), bool),
+                      [int(m.sum()) - 1], [1], D ** -0.5)
+    assert ds.device_error() == 0
+
+
+@pytest.mark.parametrize("T,Hq,H,D", SHAPES)
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("key", [float("inf"), float("nan")])
+def test_scores_of_infinity_or_nan(dev, T, Hq, H, D, wide, key):
+    """One cached key of one K/V head with such a score: the nodes of its row and its heads get NaN, all else is as it was."""
+    rng = np.random.default_rng(T)
+    q, a, *_ = ta._setup(rng, dev, 2, T, Hq, H, D, 16, [2500, 900] if wide else [130, 150], torch.bfloat16)
+    if wide:
+        a = ta._widen(a)
+    q[..., 0] = q[..., 0].abs() + 1
+    first, l1 = ds.tree_attn(q, want_lse=True, **a)
+    at = 40 if not wide else 333
+    a["k_cache"][int(a["page_table"][0, at // 16]), at % 16, 0, 0] = key
+    out, lse = ds.tree_attn(q, want_lse=True, **a)
+    G = Hq // H
+    assert out[0, :, :G].isnan().all() and lse[0, :, :G].isnan().all()
+    assert torch.equal(out[0, :, G:], first[0, :, G:]) and torch.equal(lse[0, :, G:], l1[0, :, G:])
+    assert torch.equal(out[1], first[1]) and torch.equal(lse[1], l1[1]) and ds.device_error() == 0
