@@ -204,3 +204,39 @@ def test_scores_of_infinity_or_nan(dev, T, Hq, H, D, wide, key):
     assert out[0, :, :G].isnan().all() and lse[0, :, :G].isnan().all()
     assert torch.equal(out[0, :, G:], first[0, :, G:]) and torch.equal(lse[0, :, G:], l1[0, :, G:])
     assert torch.equal(out[1], first[1]) and torch.equal(lse[1], l1[1]) and ds.device_error() == 0
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("Hq,H,D", [(4, 1, 128), (8, 2, 128), (4, 1, 112), (8, 2, 80), (16, 2, 64), (8, 1, 176), (16, 2, 256)])
+@pytest.mark.parametrize("T", [1, 8, 9, 16, 17, 25, 32, 33, 64])
+def test_every_count_of_rows(dev, dt, Hq, H, D, T):
+    """Nodes times heads of a K/V head on both sides of every number that the kernel chooses by (32, 64, 128, 256), long
+    rows beside short ones, against the oracle."""
+    rng = np.random.default_rng(T * D + Hq)
+    ta._run(dev, rng, 4, T, Hq, H, D, 16, [1500, 0, 61, 300], dt, lens=[T, T, max(1, T - 1), T],
+            kind=["tree", "random", "chain"][T % 3])
+    ta._run(dev, rng, 3, T, Hq, H, D, 32, [150, 0, 97], dt, kind="random")
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("T,Hq,H,D", SHAPES + [(33, 4, 1, 128), (16, 2, 1, 64), (70, 2, 1, 112)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_unseen_infinities_and_nan_at_every_head_size(dev, dt, T, Hq, H, D, wide):
+    """Nodes that do not see a key get the same bits whether its K and V are numbers, infinities or NaN."""
+    rng = np.random.default_rng(T * D)
+    q, a, _, _, vis, seq, n = ta._setup(rng, dev, 2, T, Hq, H, D, 16, [900, 2001] if wide else [40, 77], dt, kind="random")
+    if wide:
+        a = ta._widen(a)
+    first = _bits(*ds.tree_attn(q, want_lse=True, **a))
+    tab = a["page_table"].cpu().numpy()
+    bad = sorted({0, T // 2, T - 1})
+    for b in range(2):
+        for i, j in enumerate(bad):
+            at = int(tab[b, (seq[b] + j) // 16]), (seq[b] + j) % 16
+            a["k_cache"][at] = torch.tensor([float("nan"), float("inf"), 1.0][i % 3], device=dev).to(dt)
+            a["v_cache"][at] = torch.tensor([float("inf"), -float("inf"), float("nan"), 448.0], device=dev).repeat(D // 4).to(dt)
+    got = _bits(*ds.tree_attn(q, want_lse=True, **a))
+    blind = torch.from_numpy(~vis[:, :, bad].any(2)).to(dev)
+    assert blind.any() or T < 2
+    assert torch.equal(got[0][blind], first[0][blind]) and torch.equal(got[1][blind], first[1][blind])
+    assert ds.device_error() == 0
