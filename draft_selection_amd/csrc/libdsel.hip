@@ -1263,12 +1263,13 @@ AttnKernels attn_kernels() {
 }
 template <bool E4M3>
 AttnKernels attn_pick(int64_t rows, int64_t dim) {
-    constexpr int S = E4M3 ? 64 : 32;
+    // an 8-bit tile of 64 keys and 64 columns is one LDS-DMA load for each of four waves
+    constexpr int S = E4M3 ? 64 : 32, R = E4M3 ? 4 : 8;
     if (dim <= 64)
-        return rows <= 32           ? attn_kernels<AttnCfg<E4M3, 64, 1, 1, 4, 32, 2>>()
-               : rows <= 64         ? attn_kernels<AttnCfg<E4M3, 64, 2, 1, 2, S, 2>>()
-               : rows <= 128 || E4M3 ? attn_kernels<AttnCfg<E4M3, 64, 4, 1, 1, 64, 2>>()
-                                    : attn_kernels<AttnCfg<E4M3, 64, E4M3 ? 4 : 8, 1, 1, 64, 2>>();
+        return rows <= 32    ? attn_kernels<AttnCfg<E4M3, 64, 1, 1, 4, 32, 2>>()
+               : rows <= 64  ? attn_kernels<AttnCfg<E4M3, 64, 2, 1, 2, S, 2>>()
+               : rows <= 128 ? attn_kernels<AttnCfg<E4M3, 64, 4, 1, 1, 64, 2>>()
+                             : attn_kernels<AttnCfg<E4M3, 64, R, 1, 1, 64, 2>>();
     if (dim <= 128)
         return rows <= 32    ? attn_kernels<AttnCfg<E4M3, 128, 1, 1, 4, 32, 2>>()
                : rows <= 64  ? attn_kernels<AttnCfg<E4M3, 128, 2, 1, 2, S, 2>>()

@@ -678,7 +678,9 @@ dsel_status dsel_pages_fork(const dsel_pages *pages, const int32_t *src, const d
  * of range, sets DSEL_DEVERR_PAGE and is left alone. */
 dsel_status dsel_pages_free(const dsel_pages *pages, const int32_t *which, dsel_stream_t stream);
 
-/* ABI version of this header (major * 100 + minor). */
+/* ABI version of this header (major * 100 + minor).  Calls that are added beside
+ * the others leave it as it is; a program that can do without one looks for its
+ * symbol in the library. */
 int32_t dsel_version(void);
 #define DSEL_VERSION 200
 

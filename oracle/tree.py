@@ -42,12 +42,6 @@ def accept(parent, tok, target):
     return path, out
 
 
-def rows_of(cache, table_row, n, page_size):
-    """Positions 0..n-1 of one row from ``cache [pages, page_size, heads, dim]``."""
-    return np.stack([cache[table_row[p // page_size], p % page_size] for p in range(n)]) if n else \
-        np.zeros((0,) + cache.shape[2:])
-
-
 def attend(q, K, V, sees, scale):
     """One sequence: ``q [n, Hq, D]``, ``K, V [N, H, D]`` fp64, ``sees [n, N]``.
     Returns ``out [n, Hq, D]``, ``lse [n, Hq]``, and for error bounds ``mag``, the
