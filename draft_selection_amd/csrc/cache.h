@@ -10,9 +10,10 @@
 // Every kernel here moves bytes and is bound by memory (or, at the small
 // sizes of one step, by its launch): 16 bytes per lane and access, neighbouring
 // lanes on neighbouring 16-byte vectors of a row.  Measured on an MI355X, 36
-// layers of 8 heads of 128 in bf16: 64 rows of up to 17 tokens appended in 51 us
-// (4.8 TB/s), their kept paths compacted in 13; 48 forks of 8 layers, pages of 64
-// slots, in 20 to 23 us of copying (4.5 TB/s) and 12 of handing out pages.
+// layers of 8 heads of 128 in bf16 (medians of a kernel trace): 64 rows of up to 17
+// tokens appended in 51 us (4.7 TB/s), their kept paths compacted in 13; 48 forks
+// of 8 layers, pages of 64 slots, in 24 us of copying (4.2 TB/s) and 12 of handing
+// out pages.
 #pragma once
 
 #include "common.h"
@@ -238,7 +239,7 @@ __device__ __forceinline__ uint32_t free_bits(const PoolParams &p, int64_t first
 // pages in row order, if the pool holds enough for every row; else none.
 // The pool is the refcount array itself (a page is free when its count is 0),
 // so no list has to be kept in step with it and the pages handed out depend on
-// nothing but the counts.  16 pages per thread and 16,384 per pass; 5 to 14 us,
+// nothing but the counts.  16 pages per thread and 16,384 per pass; 6 to 12 us,
 // a few dependent loads and prefix sums in one workgroup.
 // FORK: the one page of row r goes to plan[r]; else the pages follow those
 // that the row holds already.

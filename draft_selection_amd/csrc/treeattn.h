@@ -22,15 +22,16 @@
 // if V^T's keys are taken in the same order.  V lies in LDS by keys; the
 // transposing LDS reads deliver it by columns.
 //
-// Measured on an MI355X, caches in HBM, 32 query heads on 8 of 128: 64 rows of
-// up to 4,096 cached positions and chains of up to 17 nodes, 160 us and 9 for the
-// join (4.4 TB/s; the same keys moved with no arithmetic take about as long); 8
-// rows of up to 16,384 and trees of 64, 129 and 10 (560 TFLOP/s; keys alone 110,
-// products alone 130 where the kernel takes 205 at equal lengths: the waves
-// stand at their LDS-DMA loads while the matrix core is free); 2 rows of 131,000
-// in 8 bits and trees of 32, 199 and 13 (690 TFLOP/s, conversions and softmax
-// on the vector unit beside the products); one token over 333, 8.8 and 3 (a chain
-// of loads: lengths, page ids, keys).
+// Measured on an MI355X, caches in HBM, 32 query heads on 8 of 128, this kernel
+// and the join together, captured, medians: 64 rows of up to 4,096 cached
+// positions and chains of up to 17 nodes, 177 us (3.9 TB/s; the same keys moved
+// with no arithmetic take 165); 8 rows of up to 16,384 and trees of up to 64, 141
+// (510 TFLOP/s; keys alone 107, products alone 115, and at equal lengths 207, 148
+// and 156: the waves stand at their LDS-DMA loads while the matrix core is free);
+// 2 rows of 131,000 in 8 bits and trees of 32, 208 (660 TFLOP/s; keys alone 136,
+// products alone 196: every row wave converts the tile's values for itself, on
+// the vector unit that also does the softmax); one token over 333, 12.5 (a chain
+// of loads: lengths, page ids, keys; then the join).
 //
 // Keys move from the cache into a ring of two or three LDS stages by 16-byte
 // LDS-DMA loads (global_load_lds_dwordx4), one or two rounds ahead; page ids as
@@ -66,7 +67,7 @@ constexpr int kJoinWords = 8;
 // card, whole against split (32 query heads on 8 of 128): one token over 120
 // keys 11.0 us against 12.3, over 250 12.7 against 12.5, over 500 16.4 against
 // 12.6; 8 rows of 17 nodes over 120 keys 13.8 against 16.3, over 250 18.0 against
-// 18.3.
+// 18.3.  (Other heads, other head sizes and 8-bit caches were not measured.)
 constexpr int kAttnWholeKeys = 256;
 
 __device__ u32x4 g_attn_zero[1];  // what a key that is none reads (never written)
@@ -420,7 +421,9 @@ __device__ __forceinline__ void attn_weights(AttnState<C> &a, AttnScores<C> &s, 
 }
 
 // O^T += V^T P^T for column blocks nb0 .. of the wave, the weights rounded to
-// bf16.  Two operands are read together.  The branch on `special` between the
+// bf16, the matrix core's type here: half a step of 2^-8 of each weight, where the
+// output is rounded by as much once more (the sum of the weights, and lse with it,
+// stays that of the unrounded ones).  Two operands are read together.  The branch on `special` between the
 // reads and the products also keeps the compiler from reading every operand of
 // the tile ahead, which costs 60 registers and spills: without it (the special
 // case as a call of its own) the kernel took 15 to 25% longer.
