@@ -1301,7 +1301,7 @@ DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cac
     if ((st = check_cache(cache, a->batch > 0, &p.c)) != DSEL_OK) return st;
     if (cache->layers != 1 || a->q_heads < 1 || a->q_heads > DSEL_MAX_HEADS || a->q_heads % cache->heads)
         return DSEL_E_ARG;
-    if (!(a->scale > 0.0f && a->scale < __builtin_inff())) return DSEL_E_ARG;
+    if (!(a->scale > 0.0f && a->scale <= 0x1p127f)) return DSEL_E_ARG;  // times log2(e) it is finite
     if ((st = check_table(a->page_table, a->table_ld, a->max_pages, cache->page_size, a->seq_len, a->batch, a->block,
                           a->block_len, &p.t)) != DSEL_OK)
         return st;

@@ -566,7 +566,7 @@ dsel_status dsel_tree_mask(const int32_t *parent, int64_t batch, int64_t block, 
  *              * page_size: a table that holds a few hundred keys per row at most
  *              needs none, and is answered by one launch instead of two.
  * Requirements: cache->layers == 1 and cache->heads divides q_heads; q, out
- * 16-byte aligned, q's strides multiples of 8; 0 < scale < inf; table_ld >=
+ * 16-byte aligned, q's strides multiples of 8; 0 < scale <= 2^127; table_ld >=
  * max_pages. */
 typedef struct {
     const uint16_t *q;

@@ -1,4 +1,4 @@
-"""Host-side validation of the tree and cache calls: which memory they take.
+"""Host-side validation of the tree and cache calls: what memory and which scales they take.
 
 CPU only: every call below has nothing to do or fails validation."""
 import ctypes as C
@@ -59,3 +59,9 @@ def test_writers_take_k_and_v_apart_or_as_one(lib, dt, size):
     assert append(at._cache(dt=dt), F + 16) == -1
     if dt == 2:
         assert append(at._cache(dt=dt, k_scale=F, v_scale=F + 4), F) == -1
+
+
+def test_scales_past_the_largest(lib):
+    """Times log2(e) they are no finite fp32, and scores of 0 would become NaN."""
+    for scale in (2.0 ** 127 * (1 + 2.0 ** -23), 3.4e38):
+        assert at._attn(lib, scale=scale) == -1

@@ -240,3 +240,19 @@ def test_unseen_infinities_and_nan_at_every_head_size(dev, dt, T, Hq, H, D, wide
     assert blind.any() or T < 2
     assert torch.equal(got[0][blind], first[0][blind]) and torch.equal(got[1][blind], first[1][blind])
     assert ds.device_error() == 0
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("scale", [1e-45, 1e-38, 2.0 ** 127])
+@pytest.mark.parametrize("wide", [False, True])
+def test_smallest_and_largest_scale(dev, dt, scale, wide):
+    """Scales at the ends of what is taken: queries of zeros (scores of 0 at any scale), and ordinary ones at the small end, where
+    the scores are 0 to rounding; nodes with masked keys among them, and nodes that see nothing."""
+    rng = np.random.default_rng(7)
+    q, a, K, V, vis, seq, n = ta._setup(rng, dev, 2, 9, 4, 1, 64, 16, [0, 900] if wide else [0, 90], dt, kind="random",
+                                        q_std=0.0 if scale > 1 else 2.0)
+    if wide:
+        a = ta._widen(a)
+    out, lse = ds.tree_attn(q, scale=scale, want_lse=True, **a)
+    ta._check(out, lse, q, K, V, vis, seq, n, float(np.float32(scale)))
+    assert ds.device_error() == 0
