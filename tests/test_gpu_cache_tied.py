@@ -1,4 +1,4 @@
-"""The calls that write a cache, with one array as both K and V."""
+"""The cache calls and the attention with one array as both K and V."""
 import numpy as np
 import pytest
 import torch
@@ -6,6 +6,7 @@ import torch
 import draft_selection_amd as ds
 from oracle import tree as ot
 import test_gpu_cache as tc
+import test_gpu_tree_attn as ta
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +47,15 @@ def test_one_array_as_k_and_v(dev, dt, L, B, T, P, H, D):
         assert ds.pages_fork(p, t(-1, 0), a, b).tolist() == [1]
         got.append((tc._bits(a), p.table.tolist(), p.refcount.tolist()))
     assert np.array_equal(got[0][0], got[1][0]) and got[0][1:] == got[1][1:] and ds.device_error() == 0
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float8_e4m3fn])
+@pytest.mark.parametrize("ctx", [90, 2000])
+def test_attention_over_one_array(dev, dt, ctx):
+    rng = np.random.default_rng(ctx)
+    q, a, *_ = ta._setup(rng, dev, 2, 9, 8, 2, 128, 16, [ctx, 7], dt)
+    a["v_cache"] = a["k_cache"].clone()
+    want = ds.tree_attn(q, want_lse=True, **a)
+    a["v_cache"] = a["k_cache"]
+    got = ds.tree_attn(q, want_lse=True, **a)
+    assert all(torch.equal(x, y) for x, y in zip(got, want)) and ds.device_error() == 0
