@@ -380,7 +380,13 @@ __global__ __launch_bounds__(256) void pages_fork_kernel(PoolParams p, CacheView
             else device_error(kErrPage);
         }
         if (tid == 0) {
-            if (rest) to[whole] = fresh;
+            if (rest) {
+                // with no page to copy, its id is taken along and the new page goes back
+                const int page = from[whole];
+                const bool good = page >= 0 && page < p.num_pages;
+                to[whole] = good ? fresh : page;
+                if (!good) p.refcount[fresh] = 0;
+            }
             p.row_pages[r] = whole + (rest ? 1 : 0);
             p.seq_len[r] = n;
         }

@@ -664,8 +664,10 @@ dsel_status dsel_pages_reserve(const dsel_pages *pages, const int32_t *extra, in
  * in use; the rest stays as it was), so that both rows can grow.  Many rows may
  * name one source.  Pages past the source's seq_len are not taken along.  Row r
  * must hold no page and its source must not be a target itself; another entry
- * is left out and sets DSEL_DEVERR_SEQ_LEN.  All copies get their pages (the
- * lowest free ids, in row order) or none takes place, as for pages_reserve.
+ * is left out and sets DSEL_DEVERR_SEQ_LEN.  A page id of the source outside [0,
+ * num_pages) is taken along as it is and sets DSEL_DEVERR_PAGE.  All copies get
+ * their pages (the lowest free ids, in row order) or none takes place, as for
+ * pages_reserve.
  *   cache  every layer of the cache; its num_pages and page_size are the pool's.
  *   workspace  dsel_pages_fork_workspace_bytes() bytes, 4-byte aligned. */
 size_t dsel_pages_fork_workspace_bytes(int64_t rows);
