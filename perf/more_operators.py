@@ -196,7 +196,7 @@ def _quantise(x):
     """(codes, scale bytes) of values [..., dim] in the 4-bit format, two codes a byte."""
     b = x.reshape(*x.shape[:-1], -1, 32).float()
     m, k = torch.frexp(b.abs().amax(-1))
-    e = torch.where(m == 0, -125, torch.where(m <= 0.875, k - 3, k - 2)).clamp(-125, 125)
+    e = torch.where(m == 0, -123, torch.where(m <= 0.875, k - 3, k - 2)).clamp(-123, 125)
     y = b.abs() * _power(127 - e)[..., None]
     step = torch.where(y < 2, 0.5, torch.where(y < 4, 1.0, 2.0))
     y = (torch.round(y / step) * step).clamp(max=6.0)
@@ -567,7 +567,7 @@ def exact(c, seed):
     def grid4(x):
         """The nearest values of the 4-bit format, by the distance to each."""
         b = x.to(torch.float64).reshape(*x.shape[:-1], -1, 32)
-        e = torch.ceil(torch.log2(b.abs().amax(-1, keepdim=True) / 7)).clamp(-125, 125)
+        e = torch.ceil(torch.log2(b.abs().amax(-1, keepdim=True) / 7)).clamp(-123, 125)
         y = b / torch.exp2(e)
         grid = torch.tensor(GRID, dtype=torch.float64, device=DEV)
         best = torch.zeros_like(y)
