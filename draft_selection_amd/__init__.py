@@ -28,6 +28,9 @@ Entry points (same names as the C ABI):
   pages_reserve(pages, extra), pages_fork(pages, src, k_cache, v_cache)
                                                     -> granted
   pages_free(pages, which)                          (pages: a Pages tuple)
+  tree_attn_window(q, k_cache, v_cache, page_table, seq_len, window, sinks) -> out, lse
+  key_weights(q, lse, k_cache, page_table, seq_len, weights) -> weights
+  cache_evict(pages, budget, weights, k_cache, v_cache) -> granted
   device_error()                                    -> sticky device error bits
 Every batch call takes ``block_len`` (a ragged batch: valid positions per
 block, int32 on the GPU) and ``stream``.
@@ -48,7 +51,7 @@ LIB_PATH = os.path.join(_PKG, "libdsel.so")
 K = 16
 MAX_BLOCK = 32
 GREEDY, SAMPLED = 0, 1
-F32, BF16, E4M3 = 0, 1, 2
+F32, BF16, E4M3, MXFP4 = 0, 1, 2, 4
 MAX_TREE = 256
 DEVERR_TOKEN_RANGE, DEVERR_BLOCK_LEN, DEVERR_SEQ_LEN, DEVERR_PAGE, DEVERR_TREE, DEVERR_POOL = 1, 2, 4, 8, 16, 32
 
@@ -145,6 +148,11 @@ def _load():
             "dsel_pages_fork_workspace_bytes": ([I64], SZ),
             "dsel_pages_fork": ([P, P, P, P, P, SZ, P], I32),
             "dsel_pages_free": ([P, P, P], I32),
+            "dsel_tree_attn_window_workspace_bytes": ([I64, I64, I64, I64, I64, I32, I64, I64, I64], SZ),
+            "dsel_tree_attn_window": ([P, P, I64, I64, P, P, SZ, P], I32),
+            "dsel_key_weights": ([P, P, P, C.c_float, P, I64, P], I32),
+            "dsel_cache_evict_workspace_bytes": ([I64, I64, I64], SZ),
+            "dsel_cache_evict": ([P, P, P, I64, I64, I64, P, P, P, P, SZ, P], I32),
             "dsel_device_error": ([C.POINTER(C.c_int32), P], I32),
             "dsel_status_string": ([I32], C.c_char_p),
             "dsel_version": ([], I32),
@@ -732,6 +740,8 @@ _PACK_ATTN = struct.Struct("@P6qPPqqPPf4xPP").pack
 _PACK_PAGES = struct.Struct("@PqqqPPPqq").pack
 _PACK_STRIDES = struct.Struct("@4q").pack
 _I32, _F32, _BF16, _E4M3 = torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn
+_FP4, _E8M0 = torch.float4_e2m1fn_x2, torch.float8_e8m0fnu
+_CACHE_TYPES = {_BF16: BF16, _E4M3: E4M3, _FP4: MXFP4}
 
 
 def _placed(fn):
@@ -801,29 +811,48 @@ def _differ(shape, a, b):
 def _cache(dev, k, v, k_scale=None, v_scale=None):
     """Packed arguments and ``(layers, pages, page_size, heads, dim)`` of a cache
     ``[num_pages, page_size, heads, dim]`` or ``[layers, num_pages, page_size,
-    heads, dim]``: any strides (the same for K and V), the last one 1."""
+    heads, dim]``: any strides (the same for K and V), the last one 1.  A cache in
+    float4_e2m1fn_x2 has dim / 2 elements of two values each, and float8_e8m0fnu
+    scales ``[..., dim / 32]`` of the same layout (strides a 16th of the cache's)."""
     shape, sk, dt = k.shape, k.stride(), k.dtype
     if v.shape != shape or len(shape) not in (4, 5):
         raise ValueError("k_cache and v_cache must be [layers,] [num_pages, page_size, heads, dim] alike")
-    if v.dtype is not dt or (dt is not _BF16 and dt is not _E4M3):
-        raise TypeError("k_cache and v_cache must both be bfloat16 or float8_e4m3fn")
+    if v.dtype is not dt or dt not in _CACHE_TYPES:
+        raise TypeError("k_cache and v_cache must both be bfloat16, float8_e4m3fn or float4_e2m1fn_x2")
     if k.device != dev or v.device != dev:
         raise ValueError(f"the caches must be on {dev}")
     if sk[-1] != 1 or _differ(shape, sk, v.stride()):
         raise ValueError("k_cache and v_cache must have the same strides, the last one 1")
+    ps = [0, 0]
+    if dt is _FP4:
+        for i, t in enumerate((k_scale, v_scale)):
+            ps[i] = _blocks_on(dev, t, "v_scale" if i else "k_scale", shape, sk)
+        shape, sk = (*shape[:-1], shape[-1] * 2), [2 * x for x in sk]
     if len(shape) == 4:
         shape, sk, heads = (1, *shape), (0, *sk), (shape[2],)
     else:
         heads = (shape[0], shape[3])
-    ps = [0, 0]
-    for i, t in enumerate((k_scale, v_scale)):
-        if t is not None:
-            if dt is not _E4M3:
-                raise ValueError("k_scale and v_scale are for float8_e4m3fn caches")
-            ps[i] = _on(dev, t, "v_scale" if i else "k_scale", _F32, heads)
+    if dt is not _FP4:
+        for i, t in enumerate((k_scale, v_scale)):
+            if t is not None:
+                if dt is not _E4M3:
+                    raise ValueError("k_scale and v_scale are for float8_e4m3fn and float4_e2m1fn_x2 caches")
+                ps[i] = _on(dev, t, "v_scale" if i else "k_scale", _F32, heads)
     L, N, P, H, D = shape
-    return _PACK_CACHE(k.data_ptr(), v.data_ptr(), BF16 if dt is _BF16 else E4M3, L, sk[0], N, sk[1], P, sk[2], H, sk[3],
-                       D, *ps), shape
+    return _PACK_CACHE(k.data_ptr(), v.data_ptr(), _CACHE_TYPES[dt], L, sk[0], N, sk[1], P, sk[2], H, sk[3], D, *ps), shape
+
+
+def _blocks_on(dev, t, name, shape, sk):
+    """Address of the block scales of a 4-bit cache of this shape and these strides (in bytes)."""
+    if t is None or t.dtype is not _E8M0:
+        raise TypeError(f"{name} must be float8_e8m0fnu for a float4_e2m1fn_x2 cache")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if shape[-1] % 16 or t.shape != (*shape[:-1], shape[-1] // 16):
+        raise ValueError(f"{name} must be [..., dim / 32], dim a multiple of 32")
+    if any(n > 1 and x != 16 * y for n, x, y in zip(shape[:-1], sk, t.stride())) or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must have the layout of its cache: a 16th of its strides, the last one 1")
+    return t.data_ptr()
 
 
 def _cur(dev):
@@ -857,25 +886,18 @@ def tree_attn_workspace_bytes(batch: int, block: int, q_heads: int, kv_heads: in
                               max_len: int) -> int:
     """``dtype``: the cache's; ``max_len``: positions that a row of the page table holds."""
     return int(_load().dsel_tree_attn_workspace_bytes(batch, block, q_heads, kv_heads, dim,
-                                                      E4M3 if dtype is _E4M3 else BF16, max_len))
+                                                      _CACHE_TYPES.get(dtype, BF16), max_len))
 
 
-@_placed
-def tree_attn(q, k_cache, v_cache, page_table, seq_len, mask=None, block_len=None, scale=None, k_scale=None,
-              v_scale=None, out=None, lse=None, want_lse=False, workspace=None):
-    """Attention of drafted tokens over one layer of a paged cache and each other.
+def tree_attn_window_workspace_bytes(batch: int, block: int, q_heads: int, kv_heads: int, dim: int, dtype: torch.dtype,
+                                     max_len: int, window: int, sinks: int = 0) -> int:
+    return int(_load().dsel_tree_attn_window_workspace_bytes(batch, block, q_heads, kv_heads, dim, _CACHE_TYPES[dtype],
+                                                             max_len, window, sinks))
 
-    ``q [B, T, q_heads, dim]`` bf16 (any strides, the last one 1), caches
-    ``[num_pages, page_size, heads, dim]`` bf16 or float8_e4m3fn (any strides, the
-    last one 1; ``k_scale``, ``v_scale [heads]`` fp32 for the latter),
-    ``page_table [B, max_pages]``, ``seq_len [B]`` int32.  K and V of the tokens
-    are in the cache, at positions ``seq_len[b] + t``.  Every token sees the
-    ``seq_len`` cached positions, and the tokens whose bits are set in its row of
-    ``mask`` (tree_mask's layout; None: those up to itself).  ``scale`` defaults
-    to ``dim ** -0.5``.  Returns ``(out [B, T, q_heads, dim] bf16, lse [B, T,
-    q_heads] fp32 or None)``; a token that sees nothing gets 0 and -inf.  Calls of
-    the same sizes and lengths give the same bits; a row's last bits may differ
-    from those that it gets alone or beside rows of other lengths."""
+
+def _tree_attn(q, k_cache, v_cache, page_table, seq_len, mask, block_len, scale, k_scale, v_scale, out, lse, want_lse,
+               workspace, window):
+    """tree_attn (``window`` None) and tree_attn_window (``(window, sinks, depth)``)."""
     shape, sq, dev = q.shape, q.stride(), q.device
     if len(shape) != 4 or q.dtype is not _BF16:
         raise TypeError("q must be bfloat16 [B, T, q_heads, dim]")
@@ -903,7 +925,9 @@ def tree_attn(q, k_cache, v_cache, page_table, seq_len, mask=None, block_len=Non
     lib = _load()
     pw = wsb = 0
     if workspace is None:
-        wsb = lib.dsel_tree_attn_workspace_bytes(B, T, Hq, cs[3], D, BF16 if k_cache.dtype is _BF16 else E4M3, n * cs[2])
+        sizes = (B, T, Hq, cs[3], D, _CACHE_TYPES[k_cache.dtype], n * cs[2])
+        wsb = lib.dsel_tree_attn_workspace_bytes(*sizes) if window is None else \
+            lib.dsel_tree_attn_window_workspace_bytes(*sizes, window[0], window[1])
         if wsb:
             workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
             pw = workspace.data_ptr()
@@ -913,8 +937,93 @@ def tree_attn(q, k_cache, v_cache, page_table, seq_len, mask=None, block_len=Non
         pw, wsb = workspace.data_ptr(), workspace.nbytes
     a = _PACK_ATTN(q.data_ptr(), sq[0], sq[1], sq[2], B, T, Hq, _lens_on(dev, block_len, B), pt, ld, n, ps, pm,
                    D ** -0.5 if scale is None else scale, po, pl)
-    _check(lib.dsel_tree_attn(a, cache, pw, wsb, _cur(dev)), "dsel_tree_attn")
+    if window is None:
+        _check(lib.dsel_tree_attn(a, cache, pw, wsb, _cur(dev)), "dsel_tree_attn")
+    else:
+        depth = window[2]
+        pd = 0 if depth is None else _on(dev, depth, "depth", _I32, (B, T))
+        _check(lib.dsel_tree_attn_window(a, cache, window[0], window[1], pd, pw, wsb, _cur(dev)), "dsel_tree_attn_window")
     return out, lse
+
+
+@_placed
+def tree_attn(q, k_cache, v_cache, page_table, seq_len, mask=None, block_len=None, scale=None, k_scale=None,
+              v_scale=None, out=None, lse=None, want_lse=False, workspace=None):
+    """Attention of drafted tokens over one layer of a paged cache and each other.
+
+    ``q [B, T, q_heads, dim]`` bf16 (any strides, the last one 1), caches
+    ``[num_pages, page_size, heads, dim]`` bf16 or float8_e4m3fn (any strides, the
+    last one 1; ``k_scale``, ``v_scale [heads]`` fp32 for the latter), or ``[...,
+    dim / 2]`` float4_e2m1fn_x2 (``k_scale``, ``v_scale [num_pages, page_size, heads,
+    dim / 32]`` float8_e8m0fnu, laid out as their caches),
+    ``page_table [B, max_pages]``, ``seq_len [B]`` int32.  K and V of the tokens
+    are in the cache, at positions ``seq_len[b] + t``.  Every token sees the
+    ``seq_len`` cached positions, and the tokens whose bits are set in its row of
+    ``mask`` (tree_mask's layout; None: those up to itself).  ``scale`` defaults
+    to ``dim ** -0.5``.  Returns ``(out [B, T, q_heads, dim] bf16, lse [B, T,
+    q_heads] fp32 or None)``; a token that sees nothing gets 0 and -inf.  Calls of
+    the same sizes and lengths give the same bits; a row's last bits may differ
+    from those that it gets alone or beside rows of other lengths."""
+    return _tree_attn(q, k_cache, v_cache, page_table, seq_len, mask, block_len, scale, k_scale, v_scale, out, lse,
+                      want_lse, workspace, None)
+
+
+@_placed
+def tree_attn_window(q, k_cache, v_cache, page_table, seq_len, window, sinks=0, mask=None, depth=None, block_len=None,
+                     scale=None, k_scale=None, v_scale=None, out=None, lse=None, want_lse=False, workspace=None):
+    """tree_attn under a sliding window: of the keys that tree_attn would show it, a
+    token sees those whose position is less than ``window`` before its own, or below
+    ``sinks``.  Cached positions are their own; token t of row b is at ``seq_len[b] +
+    depth[b, t]`` (``depth [B, T]`` int32 as tree_mask gives it; None: t, a chain).
+    Keys that no token sees are not read."""
+    return _tree_attn(q, k_cache, v_cache, page_table, seq_len, mask, block_len, scale, k_scale, v_scale, out, lse,
+                      want_lse, workspace, (window, sinks, depth))
+
+
+@_placed
+def key_weights(q, lse, k_cache, page_table, seq_len, weights, block_len=None, count=None, decay=1.0, scale=None,
+                k_scale=None):
+    """Adds up the attention weight that each cached position gets, over tokens and
+    heads: ``weights[b, p] = decay * weights[b, p] + sum count[b, t] * exp(scale * <q, K_p>
+    - lse)`` for ``p < seq_len[b]``, in place.
+
+    ``q``, ``page_table``, ``seq_len``, ``block_len``, ``scale`` and ``k_cache`` with its
+    ``k_scale`` are those of a tree_attn call and ``lse [B, T, q_heads]`` is what it
+    returned; ``weights [B, n]`` fp32 (n at least the positions of a table row, unit
+    stride in the rows); ``count [B, T]`` fp32: what each token counts (None: 1).  Returns
+    ``weights``."""
+    shape, sq, dev = q.shape, q.stride(), q.device
+    if len(shape) != 4 or q.dtype is not _BF16:
+        raise TypeError("q must be bfloat16 [B, T, q_heads, dim]")
+    B, T, Hq, D = shape
+    if sq[3] != 1 and D > 1:
+        raise ValueError("q must have unit stride in the last dim")
+    if k_cache.dim() != 4:
+        raise ValueError("key_weights takes one layer's cache [num_pages, page_size, heads, dim]")
+    cache, cs = _cache(dev, k_cache, k_cache, k_scale, k_scale)
+    if cs[4] != D:
+        raise ValueError(f"q has head dim {D}, the cache {cs[4]}")
+    pt, ld, n, ps = _table(dev, page_table, seq_len, B)
+    pw, wld = _weights(dev, weights, B, n * cs[2])
+    a = _PACK_ATTN(q.data_ptr(), sq[0], sq[1], sq[2], B, T, Hq, _lens_on(dev, block_len, B), pt, ld, n, ps, 0,
+                   D ** -0.5 if scale is None else scale, 0, _on(dev, lse, "lse", _F32, (B, T, Hq)))
+    pc = 0 if count is None else _on(dev, count, "count", _F32, (B, T))
+    _check(_load().dsel_key_weights(a, cache, pc, decay, pw, wld, _cur(dev)), "dsel_key_weights")
+    return weights
+
+
+def _weights(dev, t, rows, n):
+    """Address and row stride of fp32 ``[rows, >= n]`` with unit stride inside a row."""
+    if t.dtype is not _F32 or t.device != dev:
+        raise TypeError(f"weights must be float32 on {dev}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < n:
+        raise ValueError(f"weights must be [{rows}, {n} or more]")
+    ld, one = t.stride()
+    if rows <= 1:
+        ld = t.shape[1]
+    if (t.shape[1] > 1 and one != 1) or ld < t.shape[1]:
+        raise ValueError("weights must have unit stride in its rows")
+    return t.data_ptr(), ld
 
 
 @_placed
@@ -948,7 +1057,8 @@ def cache_append(k_new, v_new, k_cache, v_cache, page_table, seq_len, block_len=
     ``seq_len[b] + t``): ``k_new``, ``v_new [B, T, heads, dim]`` bf16 for a cache of
     one layer, ``[layers, B, T, heads, dim]`` for one of several (any strides, the
     same for both, the last one 1).  float8_e4m3fn caches take ``x / scale``, held
-    to +-448.  ``seq_len`` is not changed."""
+    to +-448; float4_e2m1fn_x2 caches take the nearest values under a power of two for
+    every 32, which goes to ``k_scale`` and ``v_scale``.  ``seq_len`` is not changed."""
     shape, sk, dev = k_new.shape, k_new.stride(), k_new.device
     cache, cs = _cache(dev, k_cache, v_cache, k_scale, v_scale)
     if len(shape) != k_cache.dim() or v_new.shape != shape:
@@ -969,14 +1079,20 @@ def cache_append(k_new, v_new, k_cache, v_cache, page_table, seq_len, block_len=
                                      T, _lens_on(dev, block_len, B), _cur(dev)), "dsel_cache_append")
 
 
+def _moving(k_cache, k_scale, v_scale):
+    """The scales of a call that moves rows: those of 4-bit rows go with them, others stay."""
+    return (k_scale, v_scale) if k_cache.dtype is _FP4 else (None, None)
+
+
 @_placed
-def cache_compact(k_cache, v_cache, page_table, seq_len, path, n_keep, new_len=None):
+def cache_compact(k_cache, v_cache, page_table, seq_len, path, n_keep, new_len=None, k_scale=None, v_scale=None):
     """Keeps a path of the appended tokens: in every layer the rows at ``seq_len[b]
     + path[b, i]`` move to ``seq_len[b] + i`` for ``i < n_keep[b]`` (path ascends, as
     tree_accept gives it).  Returns ``new_len [B]`` int32, the rows' new lengths (a
-    given ``new_len`` shares no memory with the other arguments)."""
+    given ``new_len`` shares no memory with the other arguments).  ``k_scale`` and
+    ``v_scale`` are those of a float4_e2m1fn_x2 cache, which move too."""
     dev = k_cache.device
-    cache, _ = _cache(dev, k_cache, v_cache)
+    cache, _ = _cache(dev, k_cache, v_cache, *_moving(k_cache, k_scale, v_scale))
     B, T = path.shape
     pp, pn = _on(dev, path, "path", _I32), _on(dev, n_keep, "n_keep", _I32, (B,))
     pt, ld, n, ps = _table(dev, page_table, seq_len, B)
@@ -1009,12 +1125,13 @@ def pages_reserve(pages: Pages, extra):
 
 
 @_placed
-def pages_fork(pages: Pages, src, k_cache, v_cache):
+def pages_fork(pages: Pages, src, k_cache, v_cache, k_scale=None, v_scale=None):
     """Row r becomes a copy of row ``src[r]`` (-1: takes no part): whole pages
     shared, the partial last one copied in every layer; all rows or none.  Row r
-    must hold no page.  Returns ``granted [1]`` int32."""
+    must hold no page.  ``k_scale`` and ``v_scale`` are those of a float4_e2m1fn_x2
+    cache.  Returns ``granted [1]`` int32."""
     dev, R, a, px = _pages(pages, src, "src")
-    cache, _ = _cache(dev, k_cache, v_cache)
+    cache, _ = _cache(dev, k_cache, v_cache, *_moving(k_cache, k_scale, v_scale))
     granted = src.new_empty(1) if R else src.new_ones(1)
     ws = torch.empty_like(src)  # dsel_pages_fork_workspace_bytes(R)
     _check(_load().dsel_pages_fork(a, px, cache, granted.data_ptr(), ws.data_ptr(), 4 * R, _cur(dev)),
@@ -1027,3 +1144,38 @@ def pages_free(pages: Pages, which):
     """Rows with ``which[r] != 0`` give back every page they hold."""
     dev, _, a, px = _pages(pages, which, "which")
     _check(_load().dsel_pages_free(a, px, _cur(dev)), "dsel_pages_free")
+
+
+def cache_evict_workspace_bytes(rows: int, max_len: int, page_size: int) -> int:
+    """``max_len``: positions that a row of the page table holds."""
+    return int(_load().dsel_cache_evict_workspace_bytes(rows, max_len, page_size))
+
+
+@_placed
+def cache_evict(pages: Pages, budget, weights, k_cache, v_cache, sinks=0, recent=0, k_scale=None, v_scale=None,
+                kept=None, workspace=None):
+    """Rows with ``0 <= budget[r] < seq_len[r]`` keep ``budget[r]`` positions: the first
+    ``sinks``, the last ``recent``, and of the others those of the largest ``weights [rows,
+    n]`` (fp32, n at least the positions of a table row; ties to the lower position, NaN
+    last).  They move together, in order and in every layer, to fresh pages; the old pages
+    are given back; ``pages`` and ``weights`` are updated in place.  All rows or none.
+    ``kept [rows, n]`` int32 (as wide as ``weights``) gets the positions that were kept.
+    Returns ``granted [1]`` int32 (0 also sets DEVERR_POOL)."""
+    dev, R, a, pb = _pages(pages, budget, "budget")
+    cache, _ = _cache(dev, k_cache, v_cache, *_moving(k_cache, k_scale, v_scale))
+    n = pages.table.shape[1] * pages.page_size
+    pw, wld = _weights(dev, weights, R, n)
+    pk = 0
+    if kept is not None:
+        if kept.dtype is not _I32 or kept.device != dev or kept.shape != weights.shape or _differ(kept.shape, kept.stride(),
+                                                                                                 weights.stride()):
+            raise ValueError("kept must be int32 of the shape and strides of weights")
+        pk = kept.data_ptr()
+    granted = budget.new_empty(1) if R else budget.new_ones(1)
+    if workspace is None:
+        workspace = torch.empty(cache_evict_workspace_bytes(R, n, pages.page_size), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {dev}")
+    _check(_load().dsel_cache_evict(a, pb, pw, wld, sinks, recent, cache, pk, granted.data_ptr(), workspace.data_ptr(),
+                                    workspace.nbytes, _cur(dev)), "dsel_cache_evict")
+    return granted

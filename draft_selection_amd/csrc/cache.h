@@ -20,6 +20,8 @@
 
 namespace dsel {
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kErrTree = 16, kErrSeqLen = 4, kErrPage = 8, kErrPool = 32;
 constexpr int kMaxTree = 256;      // DSEL_MAX_TREE
 constexpr int kMaxRows = 4096;     // DSEL_MAX_ROWS
@@ -35,7 +37,8 @@ struct CacheView {
     int64_t slot_stride, head_stride;
     int64_t num_pages;
     int page_size;
-    const float *k_scale, *v_scale;  // [layers, heads] or NULL (1)
+    const float *k_scale, *v_scale;  // 8 bits: [layers, heads] or NULL (1)
+    uint8_t *k_block, *v_block;      // 4 bits: the scale byte of vector i is byte i; NULL otherwise
 };
 
 struct TableView {
@@ -101,9 +104,46 @@ __device__ __forceinline__ u32x4 to_e4m3(const u32x4 &a, const u32x4 &b, float s
     return r;
 }
 
+// 32 values in 4 bits, and their scale byte.  The scale is the least power of two
+// with max |x| <= 7 2^e: for max = 2^k m, 1 <= m < 2, that is 2^(k-2) if m <= 1.75,
+// else 2^(k-1), and is read off the largest pattern.  x / 2^e is exact; the
+// conversion instruction divides by the scale and rounds to nearest even, and holds
+// to 6.  bf16 patterns without their sign order like the values.  Subnormal inputs,
+// which are 0 under the least scale there is (they are below 2^-3 of it), are
+// cleared: the instruction makes nonzero codes of some of them.
+__device__ __forceinline__ uint32_t no_subnormals(uint32_t w) {
+    if ((w & 0x7F800000u) == 0) w &= 0x8000FFFFu;
+    if ((w & 0x7F80u) == 0) w &= 0xFFFF8000u;
+    return w;
+}
+__device__ __forceinline__ u32x4 to_mxfp4(const u32x4 (&w)[4], uint8_t *scale) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = pk_max_i16(top, w[i][j] & 0x7FFF7FFFu);
+    top = max(top & 0xFFFFu, top >> 16);
+    const bool none = top >= 0x7F80u;  // an infinity or NaN
+    const int e = min(max((int)((top >> 7) + ((top & 0x7Fu) > 0x60u)) - 2, 4), 252);
+    *scale = (uint8_t)(none ? 255 : e);
+    const float s = __uint_as_float((uint32_t)e << 23);
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t o = 0;
+        o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2, no_subnormals(w[i][0])), s, 0);
+        o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2, no_subnormals(w[i][1])), s, 1);
+        o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2, no_subnormals(w[i][2])), s, 2);
+        o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2, no_subnormals(w[i][3])), s, 3);
+        r[i] = none ? 0u : o;
+    }
+    return r;
+}
+
 // Workgroup (x, y, z): tokens [64 x, 64 x + 64) of batch row z, layer y / 2, K
-// or V by y % 2.
-template <bool E4M3>
+// or V by y % 2.  Of the cache's type.
+enum CacheType { kBf16, kE4m3, kMxfp4 };
+template <CacheType F>
 __global__ __launch_bounds__(256) void cache_append_kernel(AppendParams p) {
     __shared__ int64_t place[kAppendTokens];
     const int b = blockIdx.z, layer = blockIdx.y >> 1, isv = blockIdx.y & 1;
@@ -122,10 +162,15 @@ __global__ __launch_bounds__(256) void cache_append_kernel(AppendParams p) {
     for (uint32_t i = threadIdx.x; i < m * cols; i += 256) {
         const uint32_t t = i / cols, col = i - t * cols, h = col / vecs, e = col - h * vecs;
         if (place[t] < 0) continue;
-        const u32x4 *x = src + t * p.st + h * p.sh + (E4M3 ? 2 * e : e);
+        const u32x4 *x = src + t * p.st + h * p.sh + (F == kMxfp4 ? 4 * e : F == kE4m3 ? 2 * e : e);
+        const int64_t at = place[t] + h * p.c.head_stride + e;
         u32x4 w = x[0];
-        if constexpr (E4M3) w = to_e4m3(w, x[1], scale ? scale[layer * p.c.heads + h] : 1.0f);
-        dst[place[t] + h * p.c.head_stride + e] = w;
+        if constexpr (F == kE4m3) w = to_e4m3(w, x[1], scale ? scale[layer * p.c.heads + h] : 1.0f);
+        if constexpr (F == kMxfp4) {
+            const u32x4 all[4] = {w, x[1], x[2], x[3]};
+            w = to_mxfp4(all, (isv ? p.c.v_block : p.c.k_block) + layer * p.c.layer_stride + at);
+        }
+        dst[at] = w;
     }
 }
 
@@ -181,15 +226,29 @@ __global__ __launch_bounds__(256) void cache_compact_kernel(CompactParams p) {
     const uint32_t lk = i / cols;
     if (lk >= (uint32_t)(p.kinds * p.c.layers)) return;
     const uint32_t col = i - lk * cols, h = col / vecs, both = p.kinds - 1;
-    u32x4 *x = (u32x4 *)(lk & both ? p.c.v : p.c.k) + (lk >> both) * p.c.layer_stride + h * p.c.head_stride + (col - h * vecs);
+    const int64_t at = (lk >> both) * p.c.layer_stride + h * p.c.head_stride + (col - h * vecs);
+    u32x4 *x = (u32x4 *)(lk & both ? p.c.v : p.c.k) + at;
+    uint8_t *y = lk & both ? p.c.v_block : p.c.k_block;  // 4 bits: a vector's scale byte goes with it
+    if (y) y += at;
     for (int k = 0; k < n; k += 8) {
         u32x4 w[8];
+        uint8_t s[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (k + e < n) w[e] = x[from[k + e]];
+        if (y) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (k + e < n) s[e] = y[from[k + e]];
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (k + e < n && from[k + e] != to[k + e]) x[to[k + e]] = w[e];
+        if (y) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (k + e < n && from[k + e] != to[k + e]) y[to[k + e]] = s[e];
+        }
     }
 }
 
@@ -202,9 +261,9 @@ struct PoolParams {
     int32_t *row_pages, *seq_len, *refcount;
     int64_t num_pages;
     int page_size;
-    const int32_t *arg;  // which / src / extra, one per row
+    const int32_t *arg;  // which / src / extra / pages wanted, one per row
     int32_t *granted;    // out [1]
-    int32_t *plan;       // fork: workspace [rows]
+    int32_t *plan;       // fork: workspace [rows]; cut: [rows][max_pages]
 };
 
 // Exclusive prefix sum of one value per thread over a workgroup of 1024;
@@ -241,13 +300,16 @@ __device__ __forceinline__ uint32_t free_bits(const PoolParams &p, int64_t first
 // so no list has to be kept in step with it and the pages handed out depend on
 // nothing but the counts.  16 pages per thread and 16,384 per pass; 6 to 12 us,
 // a few dependent loads and prefix sums in one workgroup.
-// FORK: the one page of row r goes to plan[r]; else the pages follow those
-// that the row holds already.
-template <bool FORK>
+// kFork: the one page of row r goes to plan[r]; kCut: row r's arg[r] pages (none
+// if that is negative) go to its row of plan, beside those that it still holds;
+// kMore: the pages follow those that the row holds already.
+enum PoolGive { kMore, kFork, kCut };
+template <PoolGive G>
 __global__ __launch_bounds__(1024) void pool_give_kernel(PoolParams p) {
     __shared__ int start[kMaxRows], held[kMaxRows];
     __shared__ int part[17], over;
     __shared__ unsigned long long wanted;
+    constexpr bool FORK = G == kFork;
     const int tid = threadIdx.x;
     if (tid == 0) {
         over = 0;
@@ -272,7 +334,9 @@ __global__ __launch_bounds__(1024) void pool_give_kernel(PoolParams p) {
             const int have = p.row_pages[r], a = p.arg[r];
             held[r] = have;
             bool bad = false;
-            if constexpr (FORK) {
+            if constexpr (G == kCut) {
+                need[i] = max(a, 0);
+            } else if constexpr (FORK) {
                 if (a != -1) {
                     bad = a < 0 || a >= p.rows || a == r || have != 0;
                     if (!bad) {
@@ -341,6 +405,7 @@ __global__ __launch_bounds__(1024) void pool_give_kernel(PoolParams p) {
                     else hi = mid - 1;
                 }
                 if constexpr (FORK) p.plan[lo] = page;
+                else if constexpr (G == kCut) p.plan[(int64_t)lo * p.max_pages + (rank - start[lo])] = page;
                 else p.table[lo * p.ld + held[lo] + (rank - start[lo])] = page;
                 p.refcount[page] = 1;
             }
@@ -353,13 +418,13 @@ __global__ __launch_bounds__(1024) void pool_give_kernel(PoolParams p) {
         if constexpr (FORK) {
             if (!ok) p.plan[r] = -2;
             else if (!need[i]) p.plan[r] = code[i];
-        } else if (ok && need[i]) {
+        } else if (G == kMore && ok && need[i]) {
             p.row_pages[r] = held[r] + need[i];
         }
     }
 }
 
-// fork, after pool_give_kernel<true>.  Workgroup (0, r): row r's table entries
+// fork, after pool_give_kernel<kFork>.  Workgroup (0, r): row r's table entries
 // and counts; workgroup (1 + u, r): 16 slots of the partial last page, of one
 // layer's K or V.  A source row is never itself a fork's target, so nothing
 // read here is written here.
@@ -402,7 +467,10 @@ __global__ __launch_bounds__(256) void pages_fork_kernel(PoolParams p, CacheView
         if (tid == 0) device_error(kErrPage);
         return;
     }
-    u32x4 *x = (u32x4 *)(lk & 1 ? c.v : c.k) + (lk >> 1) * c.layer_stride + first * c.slot_stride;
+    const int64_t base = (lk >> 1) * c.layer_stride + first * c.slot_stride;
+    u32x4 *x = (u32x4 *)(lk & 1 ? c.v : c.k) + base;
+    uint8_t *y = lk & 1 ? c.v_block : c.k_block;  // 4 bits: the vectors' scale bytes
+    if (y) y += base;
     const u32x4 *src = x + page * c.page_stride;
     u32x4 *dst = x + fresh * c.page_stride;
     const uint32_t vecs = c.vecs, cols = vecs * c.heads;
@@ -410,6 +478,7 @@ __global__ __launch_bounds__(256) void pages_fork_kernel(PoolParams p, CacheView
         const uint32_t t = i / cols, col = i - t * cols, h = col / vecs;
         const int64_t o = t * c.slot_stride + h * c.head_stride + (col - h * vecs);
         dst[o] = src[o];
+        if (y) y[fresh * c.page_stride + o] = y[page * c.page_stride + o];
     }
 }
 

@@ -1,0 +1,168 @@
+// The attention weight of every cached position, summed over nodes and heads.
+//
+//   w_p <- decay w_p + sum_{i, h} count_i e^(scale <q_ih, K_p> - lse_ih)
+//
+// with the lse that the attention left: the softmax is known, so one product and
+// one exponential a score give it, V is not read, and no maximum runs along.
+//
+// S = Q K^T by 32 x 32 x 16 MFMA with the keys along the lanes: lane l has the
+// scores of key l % 32 with 16 of a tile's 32 rows, adds their weights up in one
+// register, and lanes l and l ^ 32 join at the end.  So a position's sum over all
+// rows and heads of a wave stays in a register.  A row's e^-lse count sits in the
+// exponent: 2^(c z - L), L = lse log2 e - log2 count, +inf for a row that counts
+// nothing; L is spread over the registers through LDS.
+//
+// A wave holds the K operand of 32 NK keys of one head, straight from the cache,
+// and runs the rows of q past it, which come from L2: K is read once.  The waves of
+// a workgroup share the heads (HS of them take every HS-th head each) and the
+// keys.  Bound by the bytes of K where there are many; by latency (lengths, page
+// ids, keys, heads) in small calls.
+#pragma once
+
+#include "treeattn4.h"
+
+namespace dsel {
+
+struct KeyWeightsParams {
+    CacheView c;
+    TableView t;
+    const char *q;  // bf16
+    int64_t sqb, sqt, sqh;
+    const float *lse, *count;  // count: NULL = 1
+    float *w;
+    int64_t ld;
+    const int32_t *len;
+    int B, T, Hq, D, group;
+    float scale;  // times log2(e)
+    float decay;
+    int page_shift;
+    int hs;  // waves that share the heads of the same keys: 4, 2 or 1 (by the heads there are)
+};
+
+template <CacheType F_, int DP_, int NK_>
+struct KeyWeightsCfg {
+    static constexpr CacheType F = F_;
+    static constexpr int DP = DP_, NK = NK_;
+    static constexpr int PER = F == kMxfp4 ? 32 : F == kE4m3 ? 16 : 8;  // values of a 16-byte vector
+    static constexpr int CH = DP / PER, KC = CH / 2;                     // vectors of a row, and of a lane
+};
+
+template <class C>
+__global__ __launch_bounds__(256, 2) void key_weights_kernel(KeyWeightsParams p) {
+    __shared__ float shift[4][32];
+    __shared__ float sums[4][C::NK * 32];
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+    const int hs = wave & (p.hs - 1), kg = wave / p.hs;
+    const int b = blockIdx.y;
+    const int n = block_len_of(p.len, b, p.T);
+    if (n == 0) return;
+    const int s = seq_len_of(p.t, b, 0, p.c.page_size);
+    const int32_t *const table = p.t.table + b * p.t.ld;
+    const bool padded = p.c.vecs < C::CH;
+    const int rows = n * p.group;
+    const int64_t keys = 4 / p.hs * 32 * C::NK;
+    for (int64_t first = blockIdx.x * keys; first < s; first += gridDim.x * keys) {
+        const int key0 = (int)first + kg * C::NK * 32;
+        int64_t place[C::NK];
+        bool good[C::NK];
+#pragma unroll
+        for (int i = 0; i < C::NK; ++i) {
+            const int64_t k = (int64_t)key0 + 32 * i + (lane & 31);
+            const uint32_t at = k < s ? (uint32_t)k : 0u;
+            const uint32_t pg = p.page_shift >= 0 ? at >> p.page_shift : at / (uint32_t)p.c.page_size;
+            const int page = table[pg];
+            const bool none = page < 0 || page >= p.c.num_pages;
+            if (k < s && none) device_error(kErrPage);
+            good[i] = k < s && !none;
+            place[i] = none ? 0 : (int64_t)page * p.c.page_stride + (int64_t)(at - pg * (uint32_t)p.c.page_size) * p.c.slot_stride;
+        }
+        float sum[C::NK];
+#pragma unroll
+        for (int i = 0; i < C::NK; ++i) sum[i] = 0.0f;
+        for (int hk = hs; hk < p.c.heads; hk += p.hs) {
+            u32x4 raw[C::NK][C::KC];
+            uint32_t byte[C::NK][C::KC];
+#pragma unroll
+            for (int i = 0; i < C::NK; ++i)
+#pragma unroll
+                for (int c = 0; c < C::KC; ++c) {
+                    const bool none = padded && 2 * c + h >= p.c.vecs;
+                    const int64_t at = place[i] + hk * p.c.head_stride + 2 * c + h;
+                    raw[i][c] = *(none ? g_attn_zero : (const u32x4 *)p.c.k + at);
+                    if constexpr (C::F == kMxfp4) byte[i][c] = *(none ? (const uint8_t *)g_attn_zero : p.c.k_block + at);
+                }
+            bf16x8 k[C::NK][C::DP / 16];
+#pragma unroll
+            for (int i = 0; i < C::NK; ++i)
+#pragma unroll
+                for (int c = 0; c < C::KC; ++c) {
+                    const u32x4 x = raw[i][c];
+                    if constexpr (C::F == kMxfp4) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) k[i][4 * c + j] = widen_fp4(x[j], block_scale(byte[i][c]));
+                    } else if constexpr (C::F == kE4m3) {
+                        k[i][2 * c] = widen_e4m3(x[0], x[1]);
+                        k[i][2 * c + 1] = widen_e4m3(x[2], x[3]);
+                    } else {
+                        k[i][c] = __builtin_bit_cast(bf16x8, x);
+                    }
+                }
+            const float c = C::F == kE4m3 && p.c.k_scale ? p.scale * p.c.k_scale[hk] : p.scale;
+            for (int r0 = 0; r0 < rows; r0 += 32) {
+                const int r = r0 + (lane & 31);
+                const bool live = r < rows;
+                const int t = live ? r / p.group : 0, head = hk * p.group + (live ? r - t * p.group : 0);
+                const uint16_t *const qr = (const uint16_t *)p.q + b * p.sqb + t * p.sqt + head * p.sqh;
+                bf16x8 q[C::DP / 16];
+#pragma unroll
+                for (int ks = 0; ks < C::DP / 16; ++ks) {
+                    constexpr int S = C::PER / 8;  // steps of the product that one vector of K feeds
+                    const int d = (2 * (ks / S) + h) * C::PER + 8 * (ks % S);
+                    q[ks] = __builtin_bit_cast(bf16x8, live && d < p.D ? *(const u32x4 *)(qr + d) : u32x4{0, 0, 0, 0});
+                }
+                float L = __builtin_inff();
+                if (live) {
+                    const float l = p.lse[((int64_t)b * p.T + t) * p.Hq + head];
+                    const float a = p.count ? p.count[(int64_t)b * p.T + t] : 1.0f;
+                    if (fabsf(l) < __builtin_inff() && a > 0.0f) L = l * 1.44269504088896341f - __builtin_amdgcn_logf(a);
+                }
+                if (h == 0) shift[wave][lane] = L;
+                asm volatile("" ::: "memory");
+                floatx4 Ls[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) Ls[j] = *(const floatx4 *)&shift[wave][8 * j + 4 * h];
+#pragma unroll
+                for (int i = 0; i < C::NK; ++i) {
+                    floatx16 z = {};
+#pragma unroll
+                    for (int ks = 0; ks < C::DP / 16; ++ks) z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[ks], k[i][ks], z, 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float x = Ls[e >> 2][e & 3];
+                        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(z[e], c, -x));
+                        sum[i] += x < __builtin_inff() ? y : 0.0f;
+                    }
+                }
+                asm volatile("" ::: "memory");
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < C::NK; ++i) {
+            sum[i] += __uint_as_float(xor_lane32<32>(__float_as_uint(sum[i])));
+            if (h == 0) sums[wave][32 * i + lane] = sum[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < C::NK; ++i) {
+            if (hs != 0 || h != 0) break;
+            float x = sum[i];
+            for (int k = 1; k < p.hs; ++k) x += sums[wave + k][32 * i + lane];
+            if (!good[i]) continue;
+            float *w = p.w + b * p.ld + key0 + 32 * i + lane;
+            *w = p.decay == 0.0f ? x : __builtin_fmaf(p.decay, *w, x);
+        }
+        __syncthreads();  // the sums are read
+    }
+}
+
+}  // namespace dsel

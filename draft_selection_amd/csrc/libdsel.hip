@@ -11,7 +11,9 @@
 #include "dsel.h"
 #include "common.h"
 #include "conv.h"
+#include "evict.h"
 #include "fused.h"
+#include "keyweights.h"
 #include "latency.h"
 #include "lmhead.h"
 #include "pairwalk.h"
@@ -20,6 +22,7 @@
 #include "topk16.h"
 #include "tree.h"
 #include "treeattn.h"
+#include "treeattn4.h"
 #include "verify.h"
 
 #define DSEL_API extern "C" __attribute__((visibility("default")))
@@ -1134,22 +1137,26 @@ DSEL_API dsel_status dsel_dyn_conv(const uint16_t *x, const uint16_t *x_prev, co
 
 namespace {
 
+bool is_cache_type(dsel_dtype dt) { return dt == DSEL_BF16 || dt == DSEL_E4M3 || dt == DSEL_MXFP4; }
+
 // Checks a cache and lays its strides out in 16-byte vectors.  A stride of an
 // extent of one is never used and may be anything; so may the pointers of a call
 // with no work.
 dsel_status check_cache(const dsel_cache *c, bool work, CacheView *v) {
     if (!c) return DSEL_E_ARG;
-    if (c->dt != DSEL_BF16 && c->dt != DSEL_E4M3) return DSEL_E_DTYPE;
-    const int64_t es = c->dt == DSEL_BF16 ? 2 : 1, per = 16 / es;
+    if (!is_cache_type(c->dt)) return DSEL_E_DTYPE;
+    const bool fp4 = c->dt == DSEL_MXFP4;
+    const int64_t per = c->dt == DSEL_BF16 ? 8 : fp4 ? 32 : 16;
     if (c->layers < 1 || c->layers > DSEL_MAX_LAYERS || c->heads < 1 || c->heads > DSEL_MAX_HEADS || c->dim < 1 ||
         c->dim > DSEL_MAX_HEAD_DIM || c->num_pages < 1 || c->num_pages > INT_MAX || c->page_size < 1 ||
         c->page_size > DSEL_MAX_PAGE)
         return DSEL_E_ARG;
     if (work && (!c->k || !c->v)) return DSEL_E_ARG;
     if (c->dt == DSEL_BF16 && (c->k_scale || c->v_scale)) return DSEL_E_ARG;
+    if (work && fp4 && (!c->k_block || !c->v_block)) return DSEL_E_ARG;
     if (c->dim % per) return DSEL_E_ALIGN;
-    if (work && (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)))
-        return DSEL_E_ALIGN;
+    if (work && (!aligned(c->k, 16) || !aligned(c->v, 16))) return DSEL_E_ALIGN;
+    if (work && !fp4 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))) return DSEL_E_ALIGN;
     const int64_t extent[4] = {c->layers, c->num_pages, c->page_size, c->heads};
     const int64_t stride[4] = {c->layer_stride, c->page_stride, c->slot_stride, c->head_stride};
     int64_t st[4], reach = 0;
@@ -1172,16 +1179,22 @@ dsel_status check_cache(const dsel_cache *c, bool work, CacheView *v) {
     v->head_stride = st[3];
     v->num_pages = c->num_pages;
     v->page_size = (int)c->page_size;
-    v->k_scale = c->k_scale;
-    v->v_scale = c->v_scale;
+    v->k_scale = fp4 ? nullptr : c->k_scale;
+    v->v_scale = fp4 ? nullptr : c->v_scale;
+    v->k_block = fp4 ? c->k_block : nullptr;
+    v->v_block = fp4 ? c->v_block : nullptr;
     return DSEL_OK;
 }
 
 // K and V of a cache that is written, whose K and V go to different workgroups:
-// two arrays, or one as both (`tied`) whose rows are then the same for both.
+// two arrays, or one as both (`tied`) whose rows are then the same for both.  The
+// scale bytes of 4-bit caches go with them.
 dsel_status check_kv(const dsel_cache *c, bool tied) {
-    const int64_t row = c->dim * (c->dt == DSEL_BF16 ? 2 : 1);
-    return overlap(c->k, row, c->v, row) && !(tied && c->k == c->v) ? DSEL_E_ARG : DSEL_OK;
+    const bool fp4 = c->dt == DSEL_MXFP4, one = tied && c->k == c->v;
+    const int64_t row = fp4 ? c->dim / 2 : c->dim * (c->dt == DSEL_BF16 ? 2 : 1);
+    if (fp4 && (one ? c->k_block != c->v_block : overlap(c->k_block, c->dim / 32, c->v_block, c->dim / 32)))
+        return DSEL_E_ARG;
+    return overlap(c->k, row, c->v, row) && !one ? DSEL_E_ARG : DSEL_OK;
 }
 
 // The batch that reads or writes a cache through its page table
@@ -1257,43 +1270,92 @@ struct AttnKernels {
     int threads, wgs, part, join_y;
 };
 template <class C>
-AttnKernels attn_kernels() {
-    return {(const void *)tree_attn_kernel<C>, (const void *)tree_attn_join_kernel<C>, C::NT,
-            kAttnCUs * C::WGS, C::PART, AttnJoin<C>::Y};
+AttnKernels attn_kernels(const void *attn) {
+    using J = AttnJoin<C::E4M3, C::DP, C::ROWS>;
+    return {attn, (const void *)tree_attn_join_kernel<J>, C::NT, kAttnCUs * C::WGS, C::PART, J::Y};
 }
-template <bool E4M3>
+template <bool E4M3, bool WIN, int... X>
+AttnKernels attn_of() {
+    using C = AttnCfg<E4M3, WIN, X...>;
+    return attn_kernels<C>((const void *)tree_attn_kernel<C>);
+}
+template <bool WIN, int... X>
+AttnKernels attn4_of() {
+    using C = Attn4Cfg<WIN, X...>;
+    return attn_kernels<C>((const void *)tree_attn4_kernel<C>);
+}
+template <bool E4M3, bool WIN>
 AttnKernels attn_pick(int64_t rows, int64_t dim) {
     // an 8-bit tile of 64 keys and 64 columns is one LDS-DMA load for each of four waves
     constexpr int S = E4M3 ? 64 : 32, R = E4M3 ? 4 : 8;
     if (dim <= 64)
-        return rows <= 32    ? attn_kernels<AttnCfg<E4M3, 64, 1, 1, 4, 32, 2>>()
-               : rows <= 64  ? attn_kernels<AttnCfg<E4M3, 64, 2, 1, 2, S, 2>>()
-               : rows <= 128 ? attn_kernels<AttnCfg<E4M3, 64, 4, 1, 1, 64, 2>>()
-                             : attn_kernels<AttnCfg<E4M3, 64, R, 1, 1, 64, 2>>();
+        return rows <= 32    ? attn_of<E4M3, WIN, 64, 1, 1, 4, 32, 2>()
+               : rows <= 64  ? attn_of<E4M3, WIN, 64, 2, 1, 2, S, 2>()
+               : rows <= 128 ? attn_of<E4M3, WIN, 64, 4, 1, 1, 64, 2>()
+                             : attn_of<E4M3, WIN, 64, R, 1, 1, 64, 2>();
     if (dim <= 128)
-        return rows <= 32    ? attn_kernels<AttnCfg<E4M3, 128, 1, 1, 4, 32, 2>>()
-               : rows <= 64  ? attn_kernels<AttnCfg<E4M3, 128, 2, 1, 2, S, 2>>()
-               : rows <= 128 ? attn_kernels<AttnCfg<E4M3, 128, 4, 1, 1, 64, 2>>()
-                             : attn_kernels<AttnCfg<E4M3, 128, 8, 1, 1, 64, 3>>();
-    return rows <= 32   ? attn_kernels<AttnCfg<E4M3, 256, 1, 2, 2, 32, 2>>()
-           : rows <= 64 ? attn_kernels<AttnCfg<E4M3, 256, 2, 2, 1, 32, 2>>()
-                        : attn_kernels<AttnCfg<E4M3, 256, 4, 2, 1, 32, 3>>();
+        return rows <= 32    ? attn_of<E4M3, WIN, 128, 1, 1, 4, 32, 2>()
+               : rows <= 64  ? attn_of<E4M3, WIN, 128, 2, 1, 2, S, 2>()
+               : rows <= 128 ? attn_of<E4M3, WIN, 128, 4, 1, 1, 64, 2>()
+                             : attn_of<E4M3, WIN, 128, 8, 1, 1, 64, 3>();
+    return rows <= 32   ? attn_of<E4M3, WIN, 256, 1, 2, 2, 32, 2>()
+           : rows <= 64 ? attn_of<E4M3, WIN, 256, 2, 2, 1, 32, 2>()
+                        : attn_of<E4M3, WIN, 256, 4, 2, 1, 32, 3>();
+}
+template <bool WIN>
+AttnKernels attn4_pick(int64_t rows, int64_t dim) {
+    if (dim <= 64)
+        return rows <= 32   ? attn4_of<WIN, 64, 1, 1, 4, 32>()
+               : rows <= 64 ? attn4_of<WIN, 64, 2, 1, 2, 64>()
+                            : attn4_of<WIN, 64, 4, 1, 1, 64>();
+    if (dim <= 128)
+        return rows <= 32   ? attn4_of<WIN, 128, 1, 1, 4, 32>()
+               : rows <= 64 ? attn4_of<WIN, 128, 2, 1, 2, 32>()
+                            : attn4_of<WIN, 128, 4, 1, 1, 64>();
+    return rows <= 32   ? attn4_of<WIN, 256, 1, 2, 2, 32>()
+           : rows <= 64 ? attn4_of<WIN, 256, 2, 2, 1, 32>()
+                        : attn4_of<WIN, 256, 4, 2, 1, 32>();
+}
+template <bool WIN>
+AttnKernels attn_pick(dsel_dtype dt, int64_t rows, int64_t dim) {
+    return dt == DSEL_MXFP4  ? attn4_pick<WIN>(rows, dim)
+           : dt == DSEL_E4M3 ? attn_pick<true, WIN>(rows, dim)
+                             : attn_pick<false, WIN>(rows, dim);
 }
 
-}  // namespace
-
-DSEL_API size_t dsel_tree_attn_workspace_bytes(int64_t batch, int64_t block, int64_t q_heads, int64_t kv_heads,
-                                               int64_t dim, dsel_dtype dt, int64_t max_len) {
-    if (check_tree(batch, block) != DSEL_OK || batch == 0 || kv_heads < 1 || q_heads < 1 || q_heads > DSEL_MAX_HEADS ||
-        q_heads % kv_heads || dim < 1 || dim > DSEL_MAX_HEAD_DIM || (dt != DSEL_BF16 && dt != DSEL_E4M3))
-        return 0;
-    const int64_t rows = block * (q_heads / kv_heads);
-    const AttnKernels k = dt == DSEL_E4M3 ? attn_pick<true>(rows, dim) : attn_pick<false>(rows, dim);
-    return max_len <= kAttnWholeKeys ? 0 : (size_t)k.wgs * (2 * k.part + kJoinWords) * sizeof(float);
+// Workspace of an attention whose rows see `keys` positions at most
+size_t attn_workspace(const AttnKernels &k, int64_t keys) {
+    return keys <= kAttnWholeKeys ? 0 : (size_t)k.wgs * (2 * k.part + kJoinWords) * sizeof(float);
+}
+bool attn_sizes(int64_t batch, int64_t block, int64_t q_heads, int64_t kv_heads, int64_t dim, dsel_dtype dt) {
+    return check_tree(batch, block) == DSEL_OK && batch > 0 && kv_heads >= 1 && q_heads >= 1 && q_heads <= DSEL_MAX_HEADS &&
+           q_heads % kv_heads == 0 && dim >= 1 && dim <= DSEL_MAX_HEAD_DIM && is_cache_type(dt);
+}
+// What the nodes of a row see under a window, at most
+int64_t window_keys(int64_t max_len, int64_t window, int64_t sinks, int64_t block) {
+    return window >= max_len || sinks >= max_len ? max_len : max_len < window + sinks + block ? max_len : window + sinks + block;
 }
 
-DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cache *cache, void *workspace,
-                                    size_t workspace_bytes, dsel_stream_t stream) {
+// q's strides, those of extents of one as 0
+dsel_status check_q(const dsel_tree_attn_args *a, int64_t sq[3]) {
+    const int64_t extent[3] = {a->batch, a->block, a->q_heads}, stride[3] = {a->q_batch, a->q_token, a->q_head};
+    for (int i = 0; i < 3; ++i) {
+        sq[i] = 0;
+        if (extent[i] == 1) continue;
+        if (stride[i] < 0 || stride[i] > INT64_MAX / 16 / extent[i]) return DSEL_E_ARG;
+        if (stride[i] % 8) return DSEL_E_ALIGN;
+        sq[i] = stride[i];
+    }
+    return DSEL_OK;
+}
+
+int page_shift_of(int page_size) {
+    return (page_size & (page_size - 1)) == 0 ? __builtin_ctz((unsigned)page_size) : -1;
+}
+
+template <bool WIN>
+dsel_status tree_attn(const dsel_tree_attn_args *a, const dsel_cache *cache, int64_t window, int64_t sinks,
+                      const int32_t *depth, void *workspace, size_t workspace_bytes, dsel_stream_t stream) {
     if (!a) return DSEL_E_ARG;
     dsel_status st = check_tree(a->batch, a->block);
     if (st != DSEL_OK) return st;
@@ -1302,23 +1364,19 @@ DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cac
     if (cache->layers != 1 || a->q_heads < 1 || a->q_heads > DSEL_MAX_HEADS || a->q_heads % cache->heads)
         return DSEL_E_ARG;
     if (!(a->scale > 0.0f && a->scale <= 0x1p127f)) return DSEL_E_ARG;  // times log2(e) it is finite
+    if (WIN && (window < 1 || sinks < 0)) return DSEL_E_ARG;
     if ((st = check_table(a->page_table, a->table_ld, a->max_pages, cache->page_size, a->seq_len, a->batch, a->block,
                           a->block_len, &p.t)) != DSEL_OK)
         return st;
     if (a->batch == 0) return DSEL_OK;
     if (!a->q || !a->out) return DSEL_E_ARG;
-    if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->lse, 4) || !aligned(a->mask, 4)) return DSEL_E_ALIGN;
-    const int64_t extent[3] = {a->batch, a->block, a->q_heads}, stride[3] = {a->q_batch, a->q_token, a->q_head};
+    if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->lse, 4) || !aligned(a->mask, 4) || !aligned(depth, 4))
+        return DSEL_E_ALIGN;
     int64_t sq[3];
-    for (int i = 0; i < 3; ++i) {
-        sq[i] = 0;
-        if (extent[i] == 1) continue;
-        if (stride[i] < 0 || stride[i] > INT64_MAX / 16 / extent[i]) return DSEL_E_ARG;
-        if (stride[i] % 8) return DSEL_E_ALIGN;
-        sq[i] = stride[i];
-    }
-    const size_t need = dsel_tree_attn_workspace_bytes(a->batch, a->block, a->q_heads, cache->heads, cache->dim, cache->dt,
-                                                       a->max_pages * cache->page_size);
+    if ((st = check_q(a, sq)) != DSEL_OK) return st;
+    const int64_t rows = a->block * (a->q_heads / cache->heads), max_len = a->max_pages * cache->page_size;
+    const AttnKernels k = attn_pick<WIN>(cache->dt, rows, cache->dim);
+    const size_t need = attn_workspace(k, WIN ? window_keys(max_len, window, sinks, a->block) : max_len);
     if (need && (!workspace || workspace_bytes < need)) return DSEL_E_WORKSPACE;
     if (need && !aligned(workspace, 16)) return DSEL_E_ALIGN;
     p.q = (const char *)a->q;
@@ -1336,16 +1394,43 @@ DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cac
     p.group = (int)(a->q_heads / cache->heads);
     p.words = (int)(a->block + 31) / 32;
     p.scale = (float)((double)a->scale * 1.4426950408889634);
-    p.page_shift = (p.c.page_size & (p.c.page_size - 1)) == 0 ? __builtin_ctz((unsigned)p.c.page_size) : -1;
+    p.window = (int)(window < INT_MAX ? window : INT_MAX);
+    p.sinks = (int)(sinks < INT_MAX ? sinks : INT_MAX);
+    p.depth = depth;
+    p.page_shift = page_shift_of(p.c.page_size);
     p.part = (float *)workspace;
-    const int64_t rows = a->block * p.group;
-    const AttnKernels k = cache->dt == DSEL_E4M3 ? attn_pick<true>(rows, cache->dim) : attn_pick<false>(rows, cache->dim);
     p.wgs = k.wgs;
     p.whole = need == 0;
     p.join = (int32_t *)(p.part + (int64_t)k.wgs * 2 * k.part);
     st = launch(k.attn, dim3((unsigned)k.wgs), dim3((unsigned)k.threads), &p, 0, stream);
     if (st != DSEL_OK || p.whole) return st;
     return launch(k.join, dim3((unsigned)k.wgs, (unsigned)k.join_y), dim3(256), &p, 0, stream);
+}
+
+}  // namespace
+
+DSEL_API size_t dsel_tree_attn_workspace_bytes(int64_t batch, int64_t block, int64_t q_heads, int64_t kv_heads,
+                                               int64_t dim, dsel_dtype dt, int64_t max_len) {
+    if (!attn_sizes(batch, block, q_heads, kv_heads, dim, dt)) return 0;
+    return attn_workspace(attn_pick<false>(dt, block * (q_heads / kv_heads), dim), max_len);
+}
+
+DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cache *cache, void *workspace,
+                                    size_t workspace_bytes, dsel_stream_t stream) {
+    return tree_attn<false>(a, cache, 1, 0, nullptr, workspace, workspace_bytes, stream);
+}
+
+DSEL_API size_t dsel_tree_attn_window_workspace_bytes(int64_t batch, int64_t block, int64_t q_heads, int64_t kv_heads,
+                                                      int64_t dim, dsel_dtype dt, int64_t max_len, int64_t window,
+                                                      int64_t sinks) {
+    if (!attn_sizes(batch, block, q_heads, kv_heads, dim, dt) || window < 1 || sinks < 0) return 0;
+    return attn_workspace(attn_pick<true>(dt, block * (q_heads / kv_heads), dim), window_keys(max_len, window, sinks, block));
+}
+
+DSEL_API dsel_status dsel_tree_attn_window(const dsel_tree_attn_args *a, const dsel_cache *cache, int64_t window,
+                                           int64_t sinks, const int32_t *depth, void *workspace, size_t workspace_bytes,
+                                           dsel_stream_t stream) {
+    return tree_attn<true>(a, cache, window, sinks, depth, workspace, workspace_bytes, stream);
 }
 
 DSEL_API dsel_status dsel_cache_append(const uint16_t *k_new, const uint16_t *v_new, const int64_t strides[4],
@@ -1380,8 +1465,9 @@ DSEL_API dsel_status dsel_cache_append(const uint16_t *k_new, const uint16_t *v_
     p.T = (int)block;
     p.len = block_len;
     if ((st = check_kv(cache, k_new == v_new && cache->k_scale == cache->v_scale)) != DSEL_OK) return st;
-    const void *k = cache->dt == DSEL_E4M3 ? (const void *)cache_append_kernel<true>
-                                           : (const void *)cache_append_kernel<false>;
+    const void *k = cache->dt == DSEL_MXFP4  ? (const void *)cache_append_kernel<kMxfp4>
+                    : cache->dt == DSEL_E4M3 ? (const void *)cache_append_kernel<kE4m3>
+                                             : (const void *)cache_append_kernel<kBf16>;
     return launch(k, dim3((unsigned)((block + kAppendTokens - 1) / kAppendTokens), (unsigned)cache->layers * 2,
                           (unsigned)batch), dim3(256), &p, 0, stream);
 }
@@ -1452,7 +1538,7 @@ DSEL_API dsel_status dsel_pages_reserve(const dsel_pages *pages, const int32_t *
     if (!granted) return DSEL_E_ARG;
     if (!aligned(granted, 4)) return DSEL_E_ALIGN;
     p.granted = granted;
-    return launch((const void *)pool_give_kernel<false>, dim3(1), dim3(1024), &p, 0, stream);
+    return launch((const void *)pool_give_kernel<kMore>, dim3(1), dim3(1024), &p, 0, stream);
 }
 
 DSEL_API size_t dsel_pages_fork_workspace_bytes(int64_t rows) {
@@ -1475,7 +1561,7 @@ DSEL_API dsel_status dsel_pages_fork(const dsel_pages *pages, const int32_t *src
     if ((st = check_kv(cache, true)) != DSEL_OK) return st;
     p.granted = granted;
     p.plan = (int32_t *)workspace;
-    st = launch((const void *)pool_give_kernel<true>, dim3(1), dim3(1024), &p, 0, stream);
+    st = launch((const void *)pool_give_kernel<kFork>, dim3(1), dim3(1024), &p, 0, stream);
     if (st != DSEL_OK) return st;
     const int chunks = (c.page_size + kForkSlots - 1) / kForkSlots;
     void *args[] = {&p, &c};
@@ -1488,6 +1574,134 @@ DSEL_API dsel_status dsel_pages_free(const dsel_pages *pages, const int32_t *whi
     dsel_status st = check_pages(pages, which, &p);
     if (st != DSEL_OK || pages->rows == 0) return st;
     return launch((const void *)pages_free_kernel, dim3((unsigned)p.rows), dim3(256), &p, 0, stream);
+}
+
+// ---- key weights and eviction -------------------------------------------------
+
+namespace {
+
+template <CacheType F>
+const void *key_weights_pick(int64_t dim, int *nk) {
+    *nk = dim <= 128 ? 4 : 2;
+    return dim <= 64    ? (const void *)key_weights_kernel<KeyWeightsCfg<F, 64, 4>>
+           : dim <= 128 ? (const void *)key_weights_kernel<KeyWeightsCfg<F, 128, 4>>
+                        : (const void *)key_weights_kernel<KeyWeightsCfg<F, 256, 2>>;
+}
+
+int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
+
+// Workgroups for each of `rows` rows that a table gives `most` pieces of work at
+// most: one each, up to 2^16 in all (a piece may be as little as a few hundred
+// cycles, and most of a wide table's are none), beyond which they take several.
+int64_t wgs_for(int64_t most, int64_t rows) {
+    const int64_t cap = rows < 65536 ? 65536 / rows : 1;
+    return most < cap ? most : cap;
+}
+
+}  // namespace
+
+DSEL_API dsel_status dsel_key_weights(const dsel_tree_attn_args *a, const dsel_cache *cache, const float *count,
+                                      float decay, float *weights, int64_t weights_ld, dsel_stream_t stream) {
+    if (!a) return DSEL_E_ARG;
+    dsel_status st = check_tree(a->batch, a->block);
+    if (st != DSEL_OK) return st;
+    KeyWeightsParams p{};
+    if (!cache) return DSEL_E_ARG;
+    dsel_cache c = *cache;  // V is not looked at
+    c.v = c.k;
+    c.v_scale = c.k_scale;
+    if ((st = check_cache(&c, a->batch > 0, &p.c)) != DSEL_OK) return st;
+    if (c.layers != 1 || a->q_heads < 1 || a->q_heads > DSEL_MAX_HEADS || a->q_heads % c.heads) return DSEL_E_ARG;
+    if (!(a->scale > 0.0f && a->scale <= 0x1p127f)) return DSEL_E_ARG;
+    if (!(decay >= 0.0f && decay <= 1.0f)) return DSEL_E_ARG;
+    if ((st = check_table(a->page_table, a->table_ld, a->max_pages, c.page_size, a->seq_len, a->batch, a->block,
+                          a->block_len, &p.t)) != DSEL_OK)
+        return st;
+    const int64_t max_len = a->max_pages * c.page_size;
+    if (weights_ld < max_len || weights_ld > INT64_MAX / 8 / (a->batch + 1)) return DSEL_E_ARG;
+    if (a->batch == 0) return DSEL_OK;
+    if (!a->q || !a->lse || !weights) return DSEL_E_ARG;
+    if (!aligned(a->q, 16) || !aligned(a->lse, 4) || !aligned(count, 4) || !aligned(weights, 4)) return DSEL_E_ALIGN;
+    int64_t sq[3];
+    if ((st = check_q(a, sq)) != DSEL_OK) return st;
+    const int64_t tokens = a->batch * a->block * 4, nw = ((a->batch - 1) * weights_ld + max_len) * 4;
+    if (overlap(weights, nw, a->lse, tokens * a->q_heads) || (count && overlap(weights, nw, count, tokens)) ||
+        overlap(weights, nw, a->seq_len, a->batch * 4) || (a->block_len && overlap(weights, nw, a->block_len, a->batch * 4)) ||
+        overlap(weights, nw, a->page_table, ((a->batch - 1) * a->table_ld + a->max_pages) * 4))
+        return DSEL_E_ARG;
+    p.q = (const char *)a->q;
+    p.sqb = sq[0];
+    p.sqt = sq[1];
+    p.sqh = sq[2];
+    p.lse = a->lse;
+    p.count = count;
+    p.w = weights;
+    p.ld = weights_ld;
+    p.len = a->block_len;
+    p.B = (int)a->batch;
+    p.T = (int)a->block;
+    p.Hq = (int)a->q_heads;
+    p.D = (int)c.dim;
+    p.group = (int)(a->q_heads / c.heads);
+    p.scale = (float)((double)a->scale * 1.4426950408889634);
+    p.decay = decay;
+    p.page_shift = page_shift_of(p.c.page_size);
+    p.hs = c.heads >= 4 ? 4 : c.heads >= 2 ? 2 : 1;
+    int nk;
+    const void *k = c.dt == DSEL_MXFP4  ? key_weights_pick<kMxfp4>(c.dim, &nk)
+                    : c.dt == DSEL_E4M3 ? key_weights_pick<kE4m3>(c.dim, &nk)
+                                        : key_weights_pick<kBf16>(c.dim, &nk);
+    const int64_t keys = 4 / p.hs * 32 * nk, wgs = wgs_for((max_len + keys - 1) / keys, a->batch);
+    return launch(k, dim3((unsigned)wgs, (unsigned)a->batch), dim3(256), &p, 0, stream);
+}
+
+// The workspace: pages wanted [rows], the pages handed out [rows][max_pages] and
+// the positions kept [rows][max_len], each rounded up to 16 bytes.
+DSEL_API size_t dsel_cache_evict_workspace_bytes(int64_t rows, int64_t max_len, int64_t page_size) {
+    if (rows <= 0 || rows > DSEL_MAX_ROWS || page_size < 1 || page_size > DSEL_MAX_PAGE || max_len < page_size ||
+        max_len % page_size || max_len > INT_MAX - DSEL_MAX_PAGE)
+        return 0;
+    return (size_t)(up16(rows * 4) + up16(rows * (max_len / page_size) * 4) + up16(rows * max_len * 4));
+}
+
+DSEL_API dsel_status dsel_cache_evict(const dsel_pages *pages, const int32_t *budget, float *weights, int64_t weights_ld,
+                                      int64_t sinks, int64_t recent, const dsel_cache *cache, int32_t *kept,
+                                      int32_t *granted, void *workspace, size_t workspace_bytes, dsel_stream_t stream) {
+    EvictParams p{};
+    dsel_status st = check_pages(pages, budget, &p.g);
+    if (st != DSEL_OK) return st;
+    if ((st = check_cache(cache, pages->rows > 0, &p.c)) != DSEL_OK) return st;
+    if (cache->num_pages != pages->num_pages || cache->page_size != pages->page_size) return DSEL_E_ARG;
+    const int64_t max_len = pages->max_pages * pages->page_size;
+    if (sinks < 0 || recent < 0 || weights_ld < max_len || weights_ld > INT64_MAX / 8 / DSEL_MAX_ROWS) return DSEL_E_ARG;
+    if (pages->rows == 0) return DSEL_OK;
+    if (!weights || !granted) return DSEL_E_ARG;
+    if (!aligned(weights, 4) || !aligned(kept, 4) || !aligned(granted, 4)) return DSEL_E_ALIGN;
+    if (!workspace || workspace_bytes < dsel_cache_evict_workspace_bytes(pages->rows, max_len, pages->page_size))
+        return DSEL_E_WORKSPACE;
+    if (!aligned(workspace, 16)) return DSEL_E_ALIGN;
+    if ((st = check_kv(cache, true)) != DSEL_OK) return st;
+    p.budget = budget;
+    p.weights = weights;
+    p.ld = weights_ld;
+    p.sinks = (int)(sinks < INT_MAX ? sinks : INT_MAX);
+    p.recent = (int)(recent < INT_MAX ? recent : INT_MAX);
+    p.need = (int32_t *)workspace;
+    p.g.plan = (int32_t *)((char *)workspace + up16(pages->rows * 4));
+    p.list = kept ? kept : (int32_t *)((char *)p.g.plan + up16(pages->rows * pages->max_pages * 4));
+    p.list_ld = kept ? weights_ld : max_len;
+    p.kinds = cache->k == cache->v ? 1 : 2;
+    p.g.granted = granted;
+    if ((st = launch((const void *)evict_plan_kernel, dim3((unsigned)pages->rows), dim3(1024), &p, 0, stream)) != DSEL_OK)
+        return st;
+    PoolParams g = p.g;
+    g.arg = p.need;
+    if ((st = launch((const void *)pool_give_kernel<kCut>, dim3(1), dim3(1024), &g, 0, stream)) != DSEL_OK) return st;
+    const int64_t parts = p.kinds * cache->layers, runs = wgs_for((max_len + kEvictRows - 1) / kEvictRows, parts * pages->rows);
+    st = launch((const void *)evict_copy_kernel, dim3((unsigned)runs, (unsigned)parts, (unsigned)pages->rows), dim3(256), &p,
+                0, stream);
+    if (st != DSEL_OK) return st;
+    return launch((const void *)evict_finish_kernel, dim3((unsigned)pages->rows), dim3(1024), &p, 0, stream);
 }
 
 // ---- verify ----------------------------------------------------------------

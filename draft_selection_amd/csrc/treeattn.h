@@ -55,6 +55,8 @@ struct TreeAttnParams {
     const int32_t *len;
     int B, T, Hq, D, group, words;
     float scale;  // times log2(e)
+    int window, sinks;     // WIN: what a node sees of the positions before it
+    const int32_t *depth;  // WIN: [B, T], or NULL (node i at depth i)
     int wgs;      // workgroups that share the work
     bool whole;   // no tile is split (kAttnWholeKeys)
     int page_shift;  // log2 of the page size, -1 if it is no power of two
@@ -72,12 +74,12 @@ constexpr int kAttnWholeKeys = 256;
 
 __device__ u32x4 g_attn_zero[1];  // what a key that is none reads (never written)
 
-// E4M3: 8-bit cache; DP: padded head dim; RW waves of 32 rows, each as CW waves
+// E4M3: 8-bit cache; WIN: a sliding window with sinks; DP: padded head dim; RW waves of 32 rows, each as CW waves
 // that hold DP / CW columns of the output, by KW key groups; KT keys a tile; ST
 // ring stages
-template <bool E4M3_, int DP_, int RW_, int CW_, int KW_, int KT_, int ST_>
+template <bool E4M3_, bool WIN_, int DP_, int RW_, int CW_, int KW_, int KT_, int ST_>
 struct AttnCfg {
-    static constexpr bool E4M3 = E4M3_;
+    static constexpr bool E4M3 = E4M3_, WIN = WIN_;
     static constexpr int DP = DP_, RW = RW_, CW = CW_, KW = KW_, KT = KT_, ST = ST_;
     static constexpr int GW = RW * CW;                          // waves of a key group
     static constexpr int RB = DP * (E4M3 ? 1 : 2);              // bytes of a tile row
@@ -114,10 +116,16 @@ struct AttnCfg {
 // the same number of rounds whatever the lengths, and a tile's rounds are split
 // over as many workgroups as it takes; the partial sums of a split tile are
 // joined by tree_attn_join_kernel.
+//
+// Under a window the rounds are those that hold sinks and those from the first
+// position on that the root's window reaches; the rounds between are counted out,
+// so a row costs what its window costs, however long it is.
 struct AttnRow {
     int s, n;        // cached positions, nodes (0: nothing to do)
     int rts, rounds; // row tiles, rounds of each
     int units;       // units of a row tile: its rounds, or 1 (whole)
+    int head, skip;  // WIN: rounds from `head` on stand for `skip` later ones
+    __device__ __forceinline__ int at(int round) const { return round < head ? round : round + skip; }
 };
 template <class C>
 __device__ __forceinline__ AttnRow attn_row(const TreeAttnParams &p, int64_t b) {
@@ -127,6 +135,16 @@ __device__ __forceinline__ AttnRow attn_row(const TreeAttnParams &p, int64_t b) 
     if (r.s < 0) r.n = r.s = 0;
     r.rts = (r.n * p.group + C::ROWS - 1) / C::ROWS;
     r.rounds = (int)(((int64_t)r.s + r.n + C::ROUND - 1) / C::ROUND);
+    r.head = r.skip = 0;
+    if constexpr (C::WIN) {
+        const int first = (r.s > p.window ? r.s - p.window + 1 : 0) / C::ROUND;  // no node lies before position s
+        const int head = (int)(((int64_t)p.sinks + C::ROUND - 1) / C::ROUND);
+        if (head < first) {
+            r.head = head;
+            r.skip = first - head;
+            r.rounds -= r.skip;
+        }
+    }
     r.units = p.whole && r.rounds ? 1 : r.rounds;
     return r;
 }
@@ -175,7 +193,7 @@ struct AttnBatch {
     __device__ __forceinline__ int64_t load(const TreeAttnParams &p) {
         const int64_t c = ((int64_t)p.B + 63) / 64, b0 = lane_id() * c;
         int64_t sum = 0;
-        mine = AttnRow{0, 0, 0, 0, 0};
+        mine = AttnRow{};
         for (int64_t k = 0; k < c; ++k)
             if (b0 + k < p.B) {
                 mine = attn_row<C>(p, b0 + k);
@@ -192,6 +210,11 @@ struct AttnBatch {
         r.rts = __builtin_amdgcn_readlane(mine.rts, b);
         r.rounds = __builtin_amdgcn_readlane(mine.rounds, b);
         r.units = __builtin_amdgcn_readlane(mine.units, b);
+        r.head = r.skip = 0;
+        if constexpr (C::WIN) {
+            r.head = __builtin_amdgcn_readlane(mine.head, b);
+            r.skip = __builtin_amdgcn_readlane(mine.skip, b);
+        }
         return r;
     }
     // the row that unit u lies in, and the units before that row
@@ -202,7 +225,7 @@ struct AttnBatch {
         // that lane's own rows, 64 at a time
         for (int64_t k0 = 0; c > 1 && k0 < c; k0 += 64) {
             const int64_t k = k0 + lane_id();
-            const AttnRow r = k < c && b + k < p.B ? attn_row<C>(p, b + k) : AttnRow{0, 0, 0, 0, 0};
+            const AttnRow r = k < c && b + k < p.B ? attn_row<C>(p, b + k) : AttnRow{};
             const int64_t x = (int64_t)r.rts * p.c.heads * r.units, sum = wave_incl_scan64(x);
             const uint64_t m = ballot(at + sum > u);
             if (m) {
@@ -219,7 +242,6 @@ struct AttnBatch {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ bf16x8 widen_e4m3(uint32_t a, uint32_t b) {
     const bf16x2 w0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, 1.0f, false);
@@ -468,6 +490,133 @@ __device__ __forceinline__ uint32_t sees_of(const TreeAttnParams &p, int64_t b, 
     return x;
 }
 
+// What a workgroup has of one row tile: rounds [r0, r1) of it
+struct AttnPiece {
+    int b, hk, rt;
+    int t, head;  // the lane's row: node and query head
+    int r0, r1;
+    bool live;    // is there such a row?
+    int share;
+    int64_t u;    // the piece's first unit
+};
+// The sums of the workgroup's key groups joined, and the row tile's output, or its
+// part of it, written.
+template <class C>
+__device__ __forceinline__ void attn_finish(const TreeAttnParams &p, AttnState<C> &a, const AttnRow &row,
+                                            const AttnPiece &x, const AttnShares &shares, char *lds, int32_t *join) {
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int gw = wave % C::GW, grp = wave / C::GW, rw = gw / C::CW, nb0 = gw % C::CW * C::NB, h = lane >> 5;
+    const int b = x.b, hk = x.hk, t = x.t, head = x.head, r0 = x.r0, r1 = x.r1;
+    a.l += __uint_as_float(xor_lane32<32>(__float_as_uint(a.l)));
+    floatx4 mine[C::QUADS];  // the columns that this wave writes
+    if constexpr (C::KW > 1) {
+        // the key groups' sums, exchanged through LDS: every group joins (and
+        // writes) its part of the columns
+        floatx4 *const sums = (floatx4 *)lds + gw * 64 + lane;
+        float2 *const stats = (float2 *)(lds + C::KW * C::GW * C::NB * 4096) + gw * 64 + lane;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < C::NB * 4; ++k)
+            sums[(grp * C::NB * 4 + k) * C::GW * 64] = floatx4{a.o[k >> 2][4 * (k & 3)], a.o[k >> 2][4 * (k & 3) + 1],
+                                                             a.o[k >> 2][4 * (k & 3) + 2], a.o[k >> 2][4 * (k & 3) + 3]};
+        stats[grp * C::GW * 64] = float2{a.m, a.l};
+        __syncthreads();
+        float m = -__builtin_inff(), f[C::KW];
+        float2 st[C::KW];
+#pragma unroll
+        for (int g = 0; g < C::KW; ++g) {
+            st[g] = stats[g * C::GW * 64];
+            m = fmaxf(m, st[g].x);
+        }
+        const float ms = m == -__builtin_inff() ? 0.0f : m;
+        a.l = 0.0f;
+        a.m = m;
+#pragma unroll
+        for (int g = 0; g < C::KW; ++g) {
+            f[g] = __builtin_amdgcn_exp2f(st[g].x - ms);
+            a.l += st[g].y * f[g];
+        }
+#pragma unroll
+        for (int k = 0; k < C::QUADS; ++k) {
+            mine[k] = floatx4{0, 0, 0, 0};
+#pragma unroll
+            for (int g = 0; g < C::KW; ++g)
+                mine[k] += sums[(g * C::NB * 4 + grp * C::QUADS + k) * C::GW * 64] * f[g];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < C::QUADS; ++k)
+            mine[k] = floatx4{a.o[k >> 2][4 * (k & 3)], a.o[k >> 2][4 * (k & 3) + 1], a.o[k >> 2][4 * (k & 3) + 2],
+                              a.o[k >> 2][4 * (k & 3) + 3]};
+    }
+    if (threadIdx.x == 0 && r0 == 0 && r1 < row.rounds) {
+        // the tile goes on in the shares up to that of its last round
+        join[0] = b;
+        join[1] = hk;
+        join[2] = x.rt;
+        join[3] = x.share;
+        join[4] = shares.of(x.u + row.rounds - 1);
+        join[5] = row.n;
+    }
+    if (x.live) {
+        // quad k: columns 8 k + 4 h + 0..3 of the wave's part
+        const int d0 = 32 * nb0 + 8 * (grp * C::QUADS) + 4 * h;
+        const bool first = h == 0 && nb0 == 0 && grp == 0;
+        if (r0 == 0 && r1 == row.rounds) {
+            const float vs = C::E4M3 && p.c.v_scale ? p.c.v_scale[hk] : 1.0f;
+            const bool some = !(a.l <= 0.0f);  // NaN counts as something
+            const float f = some ? vs / a.l : 0.0f;
+            const int64_t at = ((int64_t)b * p.T + t) * p.Hq + head;
+#pragma unroll
+            for (int k = 0; k < C::QUADS; ++k) {
+                if (d0 + 8 * k >= p.D) continue;
+                bf16x2 y[2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e >> 1][e & 1] = (__bf16)(some ? mine[k][e] * f : 0.0f);
+                *(uint2 *)(p.out + at * p.D + d0 + 8 * k) = __builtin_bit_cast(uint2, y);
+            }
+            if (p.lse && first)
+                p.lse[at] = some ? (a.m + __builtin_amdgcn_logf(a.l)) * 0.69314718055994531f : -__builtin_inff();
+        } else {
+            float *to = p.part + (int64_t)(x.share * 2 + (r0 == 0)) * C::PART;
+            const int rr = rw * 32 + (lane & 31);
+            if (first) {
+                to[rr] = a.m;
+                to[C::ROWS + rr] = a.l;
+            }
+#pragma unroll
+            for (int k = 0; k < C::QUADS; ++k) *(floatx4 *)(to + 2 * C::ROWS + rr * C::DP + d0 + 8 * k) = mine[k];
+        }
+    }
+}
+
+// Those of the 32 keys from position `kb` on that lie at `from` or later
+__device__ __forceinline__ uint32_t keys_from(int kb, int from) {
+    return from <= kb ? ~0u : from - kb >= 32 ? 0u : ~0u << (from - kb);
+}
+__device__ __forceinline__ int depth_of(const TreeAttnParams &p, int64_t b, int t) {
+    return p.depth ? min(max(p.depth[b * p.T + t], 0), p.T - 1) : t;
+}
+// The same under a window, for a node at depth d.  Positions are compared: a
+// cached key's is its place, a node's its depth past the cached ones.  Where the
+// window holds the whole block, nodes that the mask shows are in it; a narrower
+// one over a tree looks at each node's depth.
+__device__ __forceinline__ uint32_t sees_near(const TreeAttnParams &p, int64_t b, int t, int d, int s, int kb) {
+    const uint32_t near = ~keys_from(kb, p.sinks) | keys_from(kb, s + d - p.window + 1);
+    const uint32_t w = sees_of(p, b, t, s, kb), nodes = keys_from(kb, s);
+    if (nodes == 0 || p.depth == nullptr) return w & near;
+    uint32_t close = nodes;
+    if (p.window < p.T)
+        for (uint32_t m = w & nodes; m; m &= m - 1) {
+            const int i = __builtin_ctz(m);
+            if (kb + i - s >= p.T) break;
+            const int dj = depth_of(p, b, kb + i - s);
+            if (s + dj >= p.sinks && d - dj >= p.window) close &= ~(1u << i);
+        }
+    return w & ((near & ~nodes) | close);
+}
+
 template <class C>
 __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnParams p) {
     __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
@@ -541,7 +690,9 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
         // tile, as a byte offset.  A key past the end, or of a page that is none,
         // has no place; it reads what the first key that has one reads, and its
         // score is masked.
-        auto key_pos = [&](int round) { return (uint32_t)(round * C::ROUND + grp * C::KT + (lane & (C::KT - 1))); };
+        auto key_pos = [&](int round) {
+            return (uint32_t)(row.at(round) * C::ROUND + grp * C::KT + (lane & (C::KT - 1)));
+        };
         auto page_at = [&](uint32_t k) { return p.page_shift >= 0 ? k >> p.page_shift : k / (uint32_t)p.c.page_size; };
         auto entry_of = [&](int round) -> const int32_t * {
             const uint32_t k = key_pos(round);
@@ -617,12 +768,20 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
             const uint64_t now = have[0];
 #pragma unroll
             for (int k = 0; k < A; ++k) have[k] = have[k + 1];
-            const int kb = round * C::ROUND + grp * C::KT;
-            const bool whole = kb + C::KT <= row.s && (now & kAll) == kAll;
+            const int kb = row.at(round) * C::ROUND + grp * C::KT;
+            bool whole = kb + C::KT <= row.s && (now & kAll) == kAll;
+            if constexpr (C::WIN) whole = whole && (kb + C::KT <= p.sinks || kb > row.s + p.T - 1 - p.window);
             if (idle || (now & kAll) == 0) continue;
             uint64_t see = now;
-            if (!whole)
-                see &= sees_of(p, b, t, row.s, kb) | (C::KT == 64 ? (uint64_t)sees_of(p, b, t, row.s, kb + 32) << 32 : 0);
+            if (!whole) {
+                if constexpr (C::WIN) {
+                    const int d = depth_of(p, b, t);
+                    see &= sees_near(p, b, t, d, row.s, kb) |
+                           (C::KT == 64 ? (uint64_t)sees_near(p, b, t, d, row.s, kb + 32) << 32 : 0);
+                } else {
+                    see &= sees_of(p, b, t, row.s, kb) | (C::KT == 64 ? (uint64_t)sees_of(p, b, t, row.s, kb + 32) << 32 : 0);
+                }
+            }
             const char *const vt = vring + slot(round) * C::TILE;
             AttnScores<C> s;
             attn_scores<C>(s, q, kring + slot(round) * C::TILE);
@@ -637,87 +796,8 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
             }
         }
 
-        a.l += __uint_as_float(xor_lane32<32>(__float_as_uint(a.l)));
-        floatx4 mine[C::QUADS];  // the columns that this wave writes
-        if constexpr (C::KW > 1) {
-            // the key groups' sums, exchanged through LDS: every group joins (and
-            // writes) its part of the columns
-            floatx4 *const sums = (floatx4 *)lds + gw * 64 + lane;
-            float2 *const stats = (float2 *)(lds + C::KW * C::GW * C::NB * 4096) + gw * 64 + lane;
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < C::NB * 4; ++k)
-                sums[(grp * C::NB * 4 + k) * C::GW * 64] = floatx4{a.o[k >> 2][4 * (k & 3)], a.o[k >> 2][4 * (k & 3) + 1],
-                                                                 a.o[k >> 2][4 * (k & 3) + 2], a.o[k >> 2][4 * (k & 3) + 3]};
-            stats[grp * C::GW * 64] = float2{a.m, a.l};
-            __syncthreads();
-            float m = -__builtin_inff(), f[C::KW];
-            float2 st[C::KW];
-#pragma unroll
-            for (int g = 0; g < C::KW; ++g) {
-                st[g] = stats[g * C::GW * 64];
-                m = fmaxf(m, st[g].x);
-            }
-            const float ms = m == -__builtin_inff() ? 0.0f : m;
-            a.l = 0.0f;
-            a.m = m;
-#pragma unroll
-            for (int g = 0; g < C::KW; ++g) {
-                f[g] = __builtin_amdgcn_exp2f(st[g].x - ms);
-                a.l += st[g].y * f[g];
-            }
-#pragma unroll
-            for (int k = 0; k < C::QUADS; ++k) {
-                mine[k] = floatx4{0, 0, 0, 0};
-#pragma unroll
-                for (int g = 0; g < C::KW; ++g)
-                    mine[k] += sums[(g * C::NB * 4 + grp * C::QUADS + k) * C::GW * 64] * f[g];
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < C::QUADS; ++k)
-                mine[k] = floatx4{a.o[k >> 2][4 * (k & 3)], a.o[k >> 2][4 * (k & 3) + 1], a.o[k >> 2][4 * (k & 3) + 2],
-                                  a.o[k >> 2][4 * (k & 3) + 3]};
-        }
-        if (threadIdx.x == 0 && r0 == 0 && r1 < row.rounds) {
-            // the tile goes on in the shares up to that of its last round
-            join[0] = b;
-            join[1] = hk;
-            join[2] = rt;
-            join[3] = share;
-            join[4] = shares.of(u + row.rounds - 1);
-            join[5] = row.n;
-        }
-        if (live) {
-            // quad k: columns 8 k + 4 h + 0..3 of the wave's part
-            const int d0 = 32 * nb0 + 8 * (grp * C::QUADS) + 4 * h;
-            const bool first = h == 0 && nb0 == 0 && grp == 0;
-            if (r0 == 0 && r1 == row.rounds) {
-                const float vs = C::E4M3 && p.c.v_scale ? p.c.v_scale[hk] : 1.0f;
-                const bool some = !(a.l <= 0.0f);  // NaN counts as something
-                const float f = some ? vs / a.l : 0.0f;
-                const int64_t at = ((int64_t)b * p.T + t) * p.Hq + head;
-#pragma unroll
-                for (int k = 0; k < C::QUADS; ++k) {
-                    if (d0 + 8 * k >= p.D) continue;
-                    bf16x2 y[2];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e >> 1][e & 1] = (__bf16)(some ? mine[k][e] * f : 0.0f);
-                    *(uint2 *)(p.out + at * p.D + d0 + 8 * k) = __builtin_bit_cast(uint2, y);
-                }
-                if (p.lse && first)
-                    p.lse[at] = some ? (a.m + __builtin_amdgcn_logf(a.l)) * 0.69314718055994531f : -__builtin_inff();
-            } else {
-                float *to = p.part + (int64_t)(share * 2 + (r0 == 0)) * C::PART;
-                const int rr = rw * 32 + (lane & 31);
-                if (first) {
-                    to[rr] = a.m;
-                    to[C::ROWS + rr] = a.l;
-                }
-#pragma unroll
-                for (int k = 0; k < C::QUADS; ++k) *(floatx4 *)(to + 2 * C::ROWS + rr * C::DP + d0 + 8 * k) = mine[k];
-            }
-        }
+        const AttnPiece piece{b, hk, rt, t, head, r0, r1, live, share, u};
+        attn_finish<C>(p, a, row, piece, shares, lds, join);
         u += p.whole ? 1 : r1 - r0;
         if (u < uend) {
             // the ring (and the sums in it) are read no more
@@ -732,19 +812,20 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
 // attention began and did not end; a thread takes four columns of a row and has
 // the parts of eight shares in flight at a time.  (Four rows a thread, a quarter
 // of the workgroups: 25 us instead of 14 at 2 x 131,000 keys.)
-template <class C>
+template <bool E4M3_, int DP_, int ROWS_>
 struct AttnJoin {
-    static constexpr int TR = C::DP / 4, NR = 256 / TR, Y = C::ROWS / NR;
+    static constexpr bool E4M3 = E4M3_;
+    static constexpr int DP = DP_, ROWS = ROWS_, PART = ROWS * (DP + 2);
+    static constexpr int TR = DP / 4, NR = 256 / TR, Y = ROWS / NR;
 };
 template <class C>
 __global__ __launch_bounds__(256) void tree_attn_join_kernel(TreeAttnParams p) {
-    using J = AttnJoin<C>;
     constexpr int N = 8;
     const int32_t *const join = p.join + blockIdx.x * kJoinWords;
     const int b = join[0];
     if (b < 0) return;
     const int hk = join[1], rt = join[2], w0 = join[3], w1 = join[4], n = join[5];
-    const int rr = blockIdx.y * J::NR + threadIdx.x / J::TR, d = (threadIdx.x % J::TR) * 4;
+    const int rr = blockIdx.y * C::NR + threadIdx.x / C::TR, d = (threadIdx.x % C::TR) * 4;
     const int r = rt * C::ROWS + rr;
     if (r >= n * p.group) return;
     float m = -__builtin_inff(), l = 0.0f;

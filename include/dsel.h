@@ -71,8 +71,10 @@ typedef enum {
 } dsel_status;
 
 /* E4M3 (8 bits: 4 of exponent, 3 of mantissa, largest value 448, one NaN per
- * sign, no infinity) is a type of K/V caches only. */
-typedef enum { DSEL_F32 = 0, DSEL_BF16 = 1, DSEL_E4M3 = 2 } dsel_dtype;
+ * sign, no infinity) and MXFP4 (4 bits: 2 of exponent, 1 of mantissa, the values
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign, times a power of two that 32 values
+ * share; see dsel_cache) are types of K/V caches only. */
+typedef enum { DSEL_F32 = 0, DSEL_BF16 = 1, DSEL_E4M3 = 2, DSEL_MXFP4 = 4 } dsel_dtype;
 typedef enum { DSEL_GREEDY = 0, DSEL_SAMPLED = 1 } dsel_walk_mode;
 
 /* Device error word bits (see dsel_device_error). */
@@ -462,7 +464,10 @@ dsel_status dsel_dyn_conv(const uint16_t *x, const uint16_t *x_prev, const uint1
  *   dsel_tree_attn           per layer: attention under dsel_tree_mask's bits
  *   dsel_tree_accept         which nodes the target's own tokens keep
  *   dsel_cache_compact       the kept nodes' rows moved together, all layers
- * and, between requests, dsel_pages_fork and dsel_pages_free.
+ * and, between requests, dsel_pages_fork and dsel_pages_free.  Where contexts are
+ * long, the cache may be held in 4 bits (DSEL_MXFP4), a layer may attend through
+ * dsel_tree_attn_window, and a row may be cut down by dsel_cache_evict to the
+ * positions that dsel_key_weights has seen used.
  *
  * Trees.  `block` tokens per batch row in the padded layout [batch, block], row
  * b holding block_len[b] of them (NULL: block).  Node 0 is the last verified
@@ -496,7 +501,14 @@ dsel_status dsel_dyn_conv(const uint16_t *x, const uint16_t *x_prev, const uint1
  * head * head_stride + e in both k and v (strides in elements, any order of
  * them, so tokens-first and heads-first pages, and K and V interleaved, all
  * fit).  dt is DSEL_BF16, or DSEL_E4M3 with a scale for each layer and head: an
- * element stands for its 8-bit value times the scale.
+ * element stands for its 8-bit value times the scale, or DSEL_MXFP4: element i
+ * of the layout above is the low (i even) or high four bits of byte i / 2, and
+ * stands for its 4-bit value times 2^(s - 127), where s is byte i / 32 of k_block
+ * or v_block, which so have the layout of k and v with a 32nd of its strides.  s =
+ * 255 makes its 32 elements NaN.  The calls that write such a cache write scales
+ * of 4 .. 252 and 255; what elements under 0 .. 3, 253 and 254 stand for is not
+ * defined.  (Heads-first pages, whose rows of one head lie together, are read
+ * fastest in 4 bits, where one row is half a cache line.)
  * Requirements: k, v 16-byte aligned; dim and every stride of an extent above
  * one a multiple of 16 bytes; those strides >= dim; elements of different
  * (layer, page, slot, head) distinct, and K and V apart or one and the same (k ==
@@ -512,7 +524,14 @@ typedef struct {
     int64_t page_size, slot_stride;
     int64_t heads, head_stride;
     int64_t dim;
-    const float *k_scale, *v_scale; /* [layers, heads], E4M3 only; NULL = 1 */
+    union {
+        const float *k_scale; /* E4M3: [layers, heads]; NULL = 1 */
+        uint8_t *k_block;     /* MXFP4: one byte for 32 elements, never NULL */
+    };
+    union {
+        const float *v_scale;
+        uint8_t *v_block;
+    };
 } dsel_cache;
 
 /* tree_mask -- which nodes each node sees, and how deep it lies.
@@ -586,6 +605,26 @@ size_t dsel_tree_attn_workspace_bytes(int64_t batch, int64_t block, int64_t q_he
 dsel_status dsel_tree_attn(const dsel_tree_attn_args *args, const dsel_cache *cache, void *workspace,
                            size_t workspace_bytes, dsel_stream_t stream);
 
+/* tree_attn_window -- dsel_tree_attn under a sliding window with a few first
+ * positions that stay visible: of the keys that dsel_tree_attn would show it, a
+ * node sees those whose position is below `sinks` or less than `window` before its
+ * own.  Cached position p is at p and node i at seq_len[b] + depth[b, i]:
+ *   window  >= 1: 1 sees the node's own position alone.
+ *   sinks   >= 0.
+ *   depth   [batch, block] int32 as dsel_tree_mask writes it (values are held to
+ *           0 .. block - 1); NULL: i (a chain).
+ * Keys that no node sees are not read (beyond the 32 to 256 keys that are read
+ * together).  Everything else is as for dsel_tree_attn; calls of the same window
+ * and sinks as well give the same bits.
+ *   workspace  dsel_tree_attn_window_workspace_bytes() bytes, 16-byte aligned (may
+ *              be NULL when that is 0). */
+size_t dsel_tree_attn_window_workspace_bytes(int64_t batch, int64_t block, int64_t q_heads, int64_t kv_heads,
+                                             int64_t dim, dsel_dtype dt, int64_t max_len, int64_t window,
+                                             int64_t sinks);
+dsel_status dsel_tree_attn_window(const dsel_tree_attn_args *args, const dsel_cache *cache, int64_t window,
+                                  int64_t sinks, const int32_t *depth, void *workspace, size_t workspace_bytes,
+                                  dsel_stream_t stream);
+
 /* tree_accept -- the path of the tree that the target keeps (dsel_verify's step
  * for a tree): from node 0, go to the lowest child whose token is the target's
  * token after the current node, while there is one.  With the target's arg max
@@ -612,7 +651,11 @@ dsel_status dsel_tree_accept(const int32_t *parent, const int32_t *tok, const in
  *                 l * strides[0] + b * strides[1] + t * strides[2] + h *
  *                 strides[3] + e (multiples of 8; the same for K and V).
  * E4M3 caches take x / scale (one fp32 rounding), held to +-448 and rounded to
- * nearest even.  seq_len is not changed.  The pages written must be held by
+ * nearest even.  MXFP4 caches take 32 values at a time: the power of two is the
+ * least 2^e with max |x| <= 7 2^e, -123 <= e <= 125 (so that no value is off by
+ * more than half a step of its own binade), and each x / 2^e is held to +-6 and
+ * rounded to the nearest 4-bit value, ties to an even code; an infinity or NaN
+ * among the 32 makes all of them NaN (scale byte 255, codes 0).  seq_len is not changed.  The pages written must be held by
  * their row alone, as dsel_pages_reserve and dsel_pages_fork leave them.
  * `block` may be of any length up to DSEL_MAX_APPEND here (a whole prompt). */
 dsel_status dsel_cache_append(const uint16_t *k_new, const uint16_t *v_new, const int64_t strides[4],
@@ -679,6 +722,57 @@ dsel_status dsel_pages_fork(const dsel_pages *pages, const int32_t *src, const d
  * row_pages and seq_len 0.  A page whose count is 0 already, or whose id is out
  * of range, sets DSEL_DEVERR_PAGE and is left alone. */
 dsel_status dsel_pages_free(const dsel_pages *pages, const int32_t *which, dsel_stream_t stream);
+
+/* key_weights -- the attention weight that every cached position gets, for one
+ * layer, added to what it had:
+ *   w[b][p] = decay w[b][p] + sum over nodes i and query heads h of
+ *             count[b, i] exp(scale <q_ih, K_p> - lse_ih),    p < seq_len[b].
+ * q, its strides, batch, block, q_heads, block_len, page_table, table_ld,
+ * max_pages, seq_len, scale and lse are those of the dsel_tree_attn call whose
+ * weights these are (lse is read here and required; mask and out are not looked
+ * at; an lse of dsel_tree_attn_window would count keys that its nodes did not see).
+ *   count    [batch, block] fp32 >= 0 (nullable: 1): what a node's weights count.
+ *   decay    0 <= decay <= 1.  0 writes the sums whatever w held.
+ *   weights  in and out, fp32: position p of row b at b * weights_ld + p;
+ *            weights_ld >= max_pages * page_size.
+ * Positions at or past seq_len[b] are left as they are (so a new position starts
+ * at the 0 it was cleared to), and so are positions whose page is none and rows
+ * with no nodes.  A node and head whose lse is not finite, or whose count is not
+ * above 0, counts nothing.  The cache's v and v_scale are not looked at.
+ * Arithmetic: bf16 products summed in fp32, the sums in fp32; each position is
+ * summed by one workgroup in a fixed order, so calls repeat bit for bit.
+ * Requirements: cache->layers == 1 and cache->heads divides q_heads; q 16-byte
+ * aligned, its strides multiples of 8; weights shares no memory with the inputs. */
+dsel_status dsel_key_weights(const dsel_tree_attn_args *args, const dsel_cache *cache, const float *count,
+                             float decay, float *weights, int64_t weights_ld, dsel_stream_t stream);
+
+/* cache_evict -- cuts rows of the pool down to the positions that matter: row r
+ * with 0 <= budget[r] < seq_len[r] keeps budget[r] positions, which are the first
+ * `sinks`, the last `recent`, and of the others those of the largest weight (ties
+ * to the lower position; NaN ranks below -inf, -0 equals 0).  They move together in
+ * their order, in every layer, to pages of the row's own: the lowest free page ids,
+ * in row order.  The pages that the row held are given back (another row may still
+ * hold them), its table entries, row_pages and seq_len become the new ones and
+ * entries behind them -1, and its weights move with their positions, 0 behind them
+ * up to the old length.  All rows get their pages, or, when the pool is short, none
+ * is cut: granted [1] int32 out is 1 or 0, and 0 sets DSEL_DEVERR_POOL.  (The old
+ * pages are not free before the copies are made: cut some rows at a time where the
+ * pool is nearly full.)
+ *   budget   [rows] int32: positions to keep; a row with budget[r] < 0 or >=
+ *            seq_len[r] stays as it is.  So does one with budget[r] < sinks + recent
+ *            or a length that its pages do not hold (DSEL_DEVERR_SEQ_LEN), or that
+ *            holds a page id outside [0, num_pages) (DSEL_DEVERR_PAGE).
+ *   weights  [rows][weights_ld] fp32, weights_ld >= max_pages * page_size, updated.
+ *   cache    every layer of the cache; its num_pages and page_size are the pool's.
+ *   kept     out [rows][weights_ld] int32 (nullable): the positions that row r kept,
+ *            before the move, in its first budget[r] entries (with granted 0, those
+ *            that it would have kept); other entries are not written.
+ *   workspace  dsel_cache_evict_workspace_bytes() bytes, 16-byte aligned; contents
+ *              need no initialisation.  max_len = max_pages * page_size. */
+size_t dsel_cache_evict_workspace_bytes(int64_t rows, int64_t max_len, int64_t page_size);
+dsel_status dsel_cache_evict(const dsel_pages *pages, const int32_t *budget, float *weights, int64_t weights_ld,
+                             int64_t sinks, int64_t recent, const dsel_cache *cache, int32_t *kept,
+                             int32_t *granted, void *workspace, size_t workspace_bytes, dsel_stream_t stream);
 
 /* ABI version of this header (major * 100 + minor).  Calls that are added beside
  * the others leave it as it is; a program that can do without one looks for its
