@@ -7,6 +7,7 @@
 #include <limits.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "dsel.h"
 #include "common.h"
@@ -1284,6 +1285,11 @@ AttnKernels attn4_of() {
     using C = Attn4Cfg<WIN, X...>;
     return attn_kernels<C>((const void *)tree_attn4_kernel<C>);
 }
+template <bool WIN, int... X>
+AttnKernels attn4_few_of() {
+    using C = Attn4FewCfg<WIN, X...>;
+    return attn_kernels<C>((const void *)tree_attn4_few_kernel<C>);
+}
 template <bool E4M3, bool WIN>
 AttnKernels attn_pick(int64_t rows, int64_t dim) {
     // an 8-bit tile of 64 keys and 64 columns is one LDS-DMA load for each of four waves
@@ -1305,14 +1311,17 @@ AttnKernels attn_pick(int64_t rows, int64_t dim) {
 template <bool WIN>
 AttnKernels attn4_pick(int64_t rows, int64_t dim) {
     if (dim <= 64)
-        return rows <= 32   ? attn4_of<WIN, 64, 1, 1, 4, 32>()
-               : rows <= 64 ? attn4_of<WIN, 64, 2, 1, 2, 64>()
+        return rows <= 16   ? attn4_few_of<WIN, 64, 1, 4>()
+               : rows <= 32 ? attn4_few_of<WIN, 64, 2, 4>()
+               : rows <= 64 ? attn4_of<WIN, 64, 2, 1, 2, 32>()
                             : attn4_of<WIN, 64, 4, 1, 1, 64>();
     if (dim <= 128)
-        return rows <= 32   ? attn4_of<WIN, 128, 1, 1, 4, 32>()
+        return rows <= 16   ? attn4_few_of<WIN, 128, 1, 4>()
+               : rows <= 32 ? attn4_few_of<WIN, 128, 2, 4>()
                : rows <= 64 ? attn4_of<WIN, 128, 2, 1, 2, 32>()
                             : attn4_of<WIN, 128, 4, 1, 1, 64>();
-    return rows <= 32   ? attn4_of<WIN, 256, 1, 2, 2, 32>()
+    return rows <= 16   ? attn4_few_of<WIN, 256, 1, 4>()
+           : rows <= 32 ? attn4_few_of<WIN, 256, 2, 4>()
            : rows <= 64 ? attn4_of<WIN, 256, 2, 2, 1, 32>()
                         : attn4_of<WIN, 256, 4, 2, 1, 32>();
 }

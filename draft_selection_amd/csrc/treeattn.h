@@ -39,6 +39,8 @@
 // spread what one LDS pass reads over all 64 banks.
 #pragma once
 
+#include <type_traits>
+
 #include "cache.h"
 #include "project.h"
 
@@ -820,7 +822,6 @@ struct AttnJoin {
 };
 template <class C>
 __global__ __launch_bounds__(256) void tree_attn_join_kernel(TreeAttnParams p) {
-    constexpr int N = 8;
     const int32_t *const join = p.join + blockIdx.x * kJoinWords;
     const int b = join[0];
     if (b < 0) return;
@@ -830,7 +831,8 @@ __global__ __launch_bounds__(256) void tree_attn_join_kernel(TreeAttnParams p) {
     if (r >= n * p.group) return;
     float m = -__builtin_inff(), l = 0.0f;
     floatx4 o = {0, 0, 0, 0};
-    for (int w = w0; w <= w1; w += N) {
+    auto take = [&](int w, auto count) {  // the parts of shares w .. w + N - 1
+        constexpr int N = decltype(count)::value;
         float pm[N], pl[N];
         floatx4 po[N];
 #pragma unroll
@@ -857,7 +859,10 @@ __global__ __launch_bounds__(256) void tree_attn_join_kernel(TreeAttnParams p) {
             o += po[k] * f;
         }
         m = mn;
-    }
+    };
+    if (w1 - w0 < 3) take(w0, std::integral_constant<int, 3>{});
+    else
+        for (int w = w0; w <= w1; w += 8) take(w, std::integral_constant<int, 8>{});
     const int t = r / p.group, g = r - t * p.group;
     const int64_t at = ((int64_t)b * p.T + t) * p.Hq + hk * p.group + g;
     const bool some = !(l <= 0.0f);
