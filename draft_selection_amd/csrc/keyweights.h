@@ -8,15 +8,17 @@
 // S = Q K^T by 32 x 32 x 16 MFMA with the keys along the lanes: lane l has the
 // scores of key l % 32 with 16 of a tile's 32 rows, adds their weights up in one
 // register, and lanes l and l ^ 32 join at the end.  So a position's sum over all
-// rows and heads of a wave stays in a register.  A row's e^-lse count sits in the
-// exponent: 2^(c z - L), L = lse log2 e - log2 count, +inf for a row that counts
-// nothing; L is spread over the registers through LDS.
+// rows and heads of a wave stays in a register.  The lse is subtracted before the
+// step to base 2 (its product with log2 e would be rounded at its own size, not the
+// difference's); a row that counts nothing has lse +inf.  The rows' values are spread
+// over the registers through LDS.
 //
-// A wave holds the K operand of 32 NK keys of one head, straight from the cache,
-// and runs the rows of q past it, which come from L2: K is read once.  The waves of
-// a workgroup share the heads (HS of them take every HS-th head each) and the
-// keys.  Bound by the bytes of K where there are many; by latency (lengths, page
-// ids, keys, heads) in small calls.
+// A wave holds the K operand of 64 keys of one head, straight from the cache, and
+// runs the rows of q past it, while K of its next head is on its way: K is read
+// once, q once per 64 keys from the caches.  The waves of a workgroup share the heads
+// of the same keys where there is little to do (latency: lengths, page ids, keys,
+// head by head), else each has keys of its own and they read the same q, which L1
+// then has.  Bound by the bytes of K.
 #pragma once
 
 #include "treeattn4.h"
@@ -33,22 +35,23 @@ struct KeyWeightsParams {
     int64_t ld;
     const int32_t *len;
     int B, T, Hq, D, group;
-    float scale;  // times log2(e)
-    float decay;
+    float scale, decay;
     int page_shift;
-    int hs;  // waves that share the heads of the same keys: 4, 2 or 1 (by the heads there are)
+    int hs;  // waves that share the heads of the same keys: 4, 2 or 1
 };
 
-template <CacheType F_, int DP_, int NK_>
+template <CacheType F_, int DP_>
 struct KeyWeightsCfg {
     static constexpr CacheType F = F_;
-    static constexpr int DP = DP_, NK = NK_;
+    static constexpr int DP = DP_, NK = 2;                               // 32 NK keys a wave
     static constexpr int PER = F == kMxfp4 ? 32 : F == kE4m3 ? 16 : 8;  // values of a 16-byte vector
     static constexpr int CH = DP / PER, KC = CH / 2;                     // vectors of a row, and of a lane
+    static constexpr int S = PER / 8, QS = DP / 16;                      // steps of the product that a vector feeds, and all
+    static constexpr int WAVES = DP <= 128 ? 2 : 1;                      // (two heads' K of 256 values take over 256 registers)
 };
 
 template <class C>
-__global__ __launch_bounds__(256, 2) void key_weights_kernel(KeyWeightsParams p) {
+__global__ __launch_bounds__(256, C::WAVES) void key_weights_kernel(KeyWeightsParams p) {
     __shared__ float shift[4][32];
     __shared__ float sums[4][C::NK * 32];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
@@ -58,9 +61,12 @@ __global__ __launch_bounds__(256, 2) void key_weights_kernel(KeyWeightsParams p)
     if (n == 0) return;
     const int s = seq_len_of(p.t, b, 0, p.c.page_size);
     const int32_t *const table = p.t.table + b * p.t.ld;
-    const bool padded = p.c.vecs < C::CH;
-    const int rows = n * p.group;
+    const int rows = n * p.group, last = p.c.vecs - 1;
     const int64_t keys = 4 / p.hs * 32 * C::NK;
+    struct Raw {
+        u32x4 k[C::NK][C::KC];
+        uint32_t s[C::NK][C::KC];
+    } raw[2];
     for (int64_t first = blockIdx.x * keys; first < s; first += gridDim.x * keys) {
         const int key0 = (int)first + kg * C::NK * 32;
         int64_t place[C::NK];
@@ -79,27 +85,29 @@ __global__ __launch_bounds__(256, 2) void key_weights_kernel(KeyWeightsParams p)
         float sum[C::NK];
 #pragma unroll
         for (int i = 0; i < C::NK; ++i) sum[i] = 0.0f;
-        for (int hk = hs; hk < p.c.heads; hk += p.hs) {
-            u32x4 raw[C::NK][C::KC];
-            uint32_t byte[C::NK][C::KC];
+        // Vectors past the head dim read the row's last one and meet zeros of q.
+        auto load = [&](Raw &w, int hk) {
 #pragma unroll
             for (int i = 0; i < C::NK; ++i)
 #pragma unroll
                 for (int c = 0; c < C::KC; ++c) {
-                    const bool none = padded && 2 * c + h >= p.c.vecs;
-                    const int64_t at = place[i] + hk * p.c.head_stride + 2 * c + h;
-                    raw[i][c] = *(none ? g_attn_zero : (const u32x4 *)p.c.k + at);
-                    if constexpr (C::F == kMxfp4) byte[i][c] = *(none ? (const uint8_t *)g_attn_zero : p.c.k_block + at);
+                    const int64_t at = place[i] + min(hk, p.c.heads - 1) * p.c.head_stride + min(2 * c + h, last);
+                    w.k[i][c] = ((const u32x4 *)p.c.k)[at];
+                    if constexpr (C::F == kMxfp4) w.s[i][c] = p.c.k_block[at];
                 }
-            bf16x8 k[C::NK][C::DP / 16];
+        };
+        // K of the next head is asked for behind the last q of this one: loads land in
+        // their order, and a q behind it would have to wait for it.
+        auto add = [&](const Raw &w, int hk, Raw &next) {
+            bf16x8 k[C::NK][C::QS];
 #pragma unroll
             for (int i = 0; i < C::NK; ++i)
 #pragma unroll
                 for (int c = 0; c < C::KC; ++c) {
-                    const u32x4 x = raw[i][c];
+                    const u32x4 x = w.k[i][c];
                     if constexpr (C::F == kMxfp4) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) k[i][4 * c + j] = widen_fp4(x[j], block_scale(byte[i][c]));
+                        for (int j = 0; j < 4; ++j) k[i][4 * c + j] = widen_fp4(x[j], block_scale(w.s[i][c]));
                     } else if constexpr (C::F == kE4m3) {
                         k[i][2 * c] = widen_e4m3(x[0], x[1]);
                         k[i][2 * c + 1] = widen_e4m3(x[2], x[3]);
@@ -108,23 +116,26 @@ __global__ __launch_bounds__(256, 2) void key_weights_kernel(KeyWeightsParams p)
                     }
                 }
             const float c = C::F == kE4m3 && p.c.k_scale ? p.scale * p.c.k_scale[hk] : p.scale;
-            for (int r0 = 0; r0 < rows; r0 += 32) {
+            auto tile = [&](int r0, auto last_tile) {
                 const int r = r0 + (lane & 31);
                 const bool live = r < rows;
                 const int t = live ? r / p.group : 0, head = hk * p.group + (live ? r - t * p.group : 0);
                 const uint16_t *const qr = (const uint16_t *)p.q + b * p.sqb + t * p.sqt + head * p.sqh;
-                bf16x8 q[C::DP / 16];
+                bf16x8 q[C::QS];
 #pragma unroll
-                for (int ks = 0; ks < C::DP / 16; ++ks) {
-                    constexpr int S = C::PER / 8;  // steps of the product that one vector of K feeds
-                    const int d = (2 * (ks / S) + h) * C::PER + 8 * (ks % S);
+                for (int ks = 0; ks < C::QS; ++ks) {
+                    const int d = (2 * (ks / C::S) + h) * C::PER + 8 * (ks % C::S);
                     q[ks] = __builtin_bit_cast(bf16x8, live && d < p.D ? *(const u32x4 *)(qr + d) : u32x4{0, 0, 0, 0});
                 }
                 float L = __builtin_inff();
                 if (live) {
                     const float l = p.lse[((int64_t)b * p.T + t) * p.Hq + head];
                     const float a = p.count ? p.count[(int64_t)b * p.T + t] : 1.0f;
-                    if (fabsf(l) < __builtin_inff() && a > 0.0f) L = l * 1.44269504088896341f - __builtin_amdgcn_logf(a);
+                    if (fabsf(l) < __builtin_inff() && a > 0.0f) L = p.count ? l - 0.69314718055994531f * __builtin_amdgcn_logf(a) : l;
+                }
+                if constexpr (decltype(last_tile)::value) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    load(next, hk + p.hs);
                 }
                 if (h == 0) shift[wave][lane] = L;
                 asm volatile("" ::: "memory");
@@ -135,16 +146,25 @@ __global__ __launch_bounds__(256, 2) void key_weights_kernel(KeyWeightsParams p)
                 for (int i = 0; i < C::NK; ++i) {
                     floatx16 z = {};
 #pragma unroll
-                    for (int ks = 0; ks < C::DP / 16; ++ks) z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[ks], k[i][ks], z, 0, 0, 0);
+                    for (int ks = 0; ks < C::QS; ++ks) z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[ks], k[i][ks], z, 0, 0, 0);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float x = Ls[e >> 2][e & 3];
-                        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(z[e], c, -x));
-                        sum[i] += x < __builtin_inff() ? y : 0.0f;
+                        const float x = __builtin_fmaf(z[e], c, -Ls[e >> 2][e & 3]);
+                        // a row that counts nothing may meet infinities: its NaN is no more than 0
+                        sum[i] += fmaxf(__builtin_amdgcn_exp2f(x * 1.44269504088896341f), 0.0f);
                     }
                 }
                 asm volatile("" ::: "memory");
-            }
+            };
+            int r0 = 0;
+            for (; r0 + 32 < rows; r0 += 32) tile(r0, std::integral_constant<bool, false>{});
+            tile(r0, std::integral_constant<bool, true>{});
+        };
+        load(raw[0], hs);
+        for (int hk = hs; hk < p.c.heads; hk += 2 * p.hs) {
+            add(raw[0], hk, raw[1]);
+            if (hk + p.hs >= p.c.heads) break;
+            add(raw[1], hk + p.hs, raw[0]);
         }
 #pragma unroll
         for (int i = 0; i < C::NK; ++i) {

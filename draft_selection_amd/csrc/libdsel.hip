@@ -1590,11 +1590,10 @@ DSEL_API dsel_status dsel_pages_free(const dsel_pages *pages, const int32_t *whi
 namespace {
 
 template <CacheType F>
-const void *key_weights_pick(int64_t dim, int *nk) {
-    *nk = dim <= 128 ? 4 : 2;
-    return dim <= 64    ? (const void *)key_weights_kernel<KeyWeightsCfg<F, 64, 4>>
-           : dim <= 128 ? (const void *)key_weights_kernel<KeyWeightsCfg<F, 128, 4>>
-                        : (const void *)key_weights_kernel<KeyWeightsCfg<F, 256, 2>>;
+const void *key_weights_pick(int64_t dim) {
+    return dim <= 64    ? (const void *)key_weights_kernel<KeyWeightsCfg<F, 64>>
+           : dim <= 128 ? (const void *)key_weights_kernel<KeyWeightsCfg<F, 128>>
+                        : (const void *)key_weights_kernel<KeyWeightsCfg<F, 256>>;
 }
 
 int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
@@ -1652,15 +1651,17 @@ DSEL_API dsel_status dsel_key_weights(const dsel_tree_attn_args *a, const dsel_c
     p.Hq = (int)a->q_heads;
     p.D = (int)c.dim;
     p.group = (int)(a->q_heads / c.heads);
-    p.scale = (float)((double)a->scale * 1.4426950408889634);
+    p.scale = a->scale;
     p.decay = decay;
     p.page_shift = page_shift_of(p.c.page_size);
-    p.hs = c.heads >= 4 ? 4 : c.heads >= 2 ? 2 : 1;
-    int nk;
-    const void *k = c.dt == DSEL_MXFP4  ? key_weights_pick<kMxfp4>(c.dim, &nk)
-                    : c.dt == DSEL_E4M3 ? key_weights_pick<kE4m3>(c.dim, &nk)
-                                        : key_weights_pick<kBf16>(c.dim, &nk);
-    const int64_t keys = 4 / p.hs * 32 * nk, wgs = wgs_for((max_len + keys - 1) / keys, a->batch);
+    const void *k = c.dt == DSEL_MXFP4  ? key_weights_pick<kMxfp4>(c.dim)
+                    : c.dt == DSEL_E4M3 ? key_weights_pick<kE4m3>(c.dim)
+                                        : key_weights_pick<kBf16>(c.dim);
+    // keys of their own for the waves where that still makes two workgroups a CU
+    const int64_t tiles = (max_len + 63) / 64;
+    const int most = c.heads >= 4 ? 4 : c.heads >= 2 ? 2 : 1;
+    p.hs = a->batch * tiles >= 4 * 2 * kAttnCUs ? 1 : most;
+    const int64_t keys = 4 / p.hs * 64, wgs = wgs_for((max_len + keys - 1) / keys, a->batch);
     return launch(k, dim3((unsigned)wgs, (unsigned)a->batch), dim3(256), &p, 0, stream);
 }
 
