@@ -1332,9 +1332,10 @@ AttnKernels attn_pick(dsel_dtype dt, int64_t rows, int64_t dim) {
                              : attn_pick<false, WIN>(rows, dim);
 }
 
-// Workspace of an attention whose rows see `keys` positions at most
-size_t attn_workspace(const AttnKernels &k, int64_t keys) {
-    return keys <= kAttnWholeKeys ? 0 : (size_t)k.wgs * (2 * k.part + kJoinWords) * sizeof(float);
+// Workspace of an attention whose rows see `keys` positions at most, and of which
+// rows of up to `whole` are not split
+size_t attn_workspace(const AttnKernels &k, int64_t keys, int64_t whole) {
+    return keys <= whole ? 0 : (size_t)k.wgs * (2 * k.part + kJoinWords) * sizeof(float);
 }
 bool attn_sizes(int64_t batch, int64_t block, int64_t q_heads, int64_t kv_heads, int64_t dim, dsel_dtype dt) {
     return check_tree(batch, block) == DSEL_OK && batch > 0 && kv_heads >= 1 && q_heads >= 1 && q_heads <= DSEL_MAX_HEADS &&
@@ -1385,7 +1386,8 @@ dsel_status tree_attn(const dsel_tree_attn_args *a, const dsel_cache *cache, int
     if ((st = check_q(a, sq)) != DSEL_OK) return st;
     const int64_t rows = a->block * (a->q_heads / cache->heads), max_len = a->max_pages * cache->page_size;
     const AttnKernels k = attn_pick<WIN>(cache->dt, rows, cache->dim);
-    const size_t need = attn_workspace(k, WIN ? window_keys(max_len, window, sinks, a->block) : max_len);
+    const size_t need = WIN ? attn_workspace(k, window_keys(max_len, window, sinks, a->block), kWindowWholeKeys)
+                            : attn_workspace(k, max_len, kAttnWholeKeys);
     if (need && (!workspace || workspace_bytes < need)) return DSEL_E_WORKSPACE;
     if (need && !aligned(workspace, 16)) return DSEL_E_ALIGN;
     p.q = (const char *)a->q;
@@ -1421,7 +1423,7 @@ dsel_status tree_attn(const dsel_tree_attn_args *a, const dsel_cache *cache, int
 DSEL_API size_t dsel_tree_attn_workspace_bytes(int64_t batch, int64_t block, int64_t q_heads, int64_t kv_heads,
                                                int64_t dim, dsel_dtype dt, int64_t max_len) {
     if (!attn_sizes(batch, block, q_heads, kv_heads, dim, dt)) return 0;
-    return attn_workspace(attn_pick<false>(dt, block * (q_heads / kv_heads), dim), max_len);
+    return attn_workspace(attn_pick<false>(dt, block * (q_heads / kv_heads), dim), max_len, kAttnWholeKeys);
 }
 
 DSEL_API dsel_status dsel_tree_attn(const dsel_tree_attn_args *a, const dsel_cache *cache, void *workspace,
@@ -1433,7 +1435,8 @@ DSEL_API size_t dsel_tree_attn_window_workspace_bytes(int64_t batch, int64_t blo
                                                       int64_t dim, dsel_dtype dt, int64_t max_len, int64_t window,
                                                       int64_t sinks) {
     if (!attn_sizes(batch, block, q_heads, kv_heads, dim, dt) || window < 1 || sinks < 0) return 0;
-    return attn_workspace(attn_pick<true>(dt, block * (q_heads / kv_heads), dim), window_keys(max_len, window, sinks, block));
+    return attn_workspace(attn_pick<true>(dt, block * (q_heads / kv_heads), dim), window_keys(max_len, window, sinks, block),
+                          kWindowWholeKeys);
 }
 
 DSEL_API dsel_status dsel_tree_attn_window(const dsel_tree_attn_args *a, const dsel_cache *cache, int64_t window,
@@ -1665,13 +1668,14 @@ DSEL_API dsel_status dsel_key_weights(const dsel_tree_attn_args *a, const dsel_c
     return launch(k, dim3((unsigned)wgs, (unsigned)a->batch), dim3(256), &p, 0, stream);
 }
 
-// The workspace: pages wanted [rows], the pages handed out [rows][max_pages] and
-// the positions kept [rows][max_len], each rounded up to 16 bytes.
+// The workspace: pages wanted and lengths [rows], the pages handed out [rows]
+// [max_pages], the positions kept and their weights [rows][max_len], each rounded up
+// to 16 bytes.
 DSEL_API size_t dsel_cache_evict_workspace_bytes(int64_t rows, int64_t max_len, int64_t page_size) {
     if (rows <= 0 || rows > DSEL_MAX_ROWS || page_size < 1 || page_size > DSEL_MAX_PAGE || max_len < page_size ||
         max_len % page_size || max_len > INT_MAX - DSEL_MAX_PAGE)
         return 0;
-    return (size_t)(up16(rows * 4) + up16(rows * (max_len / page_size) * 4) + up16(rows * max_len * 4));
+    return (size_t)(2 * up16(rows * 4) + up16(rows * (max_len / page_size) * 4) + 2 * up16(rows * max_len * 4));
 }
 
 DSEL_API dsel_status dsel_cache_evict(const dsel_pages *pages, const int32_t *budget, float *weights, int64_t weights_ld,
@@ -1696,9 +1700,18 @@ DSEL_API dsel_status dsel_cache_evict(const dsel_pages *pages, const int32_t *bu
     p.ld = weights_ld;
     p.sinks = (int)(sinks < INT_MAX ? sinks : INT_MAX);
     p.recent = (int)(recent < INT_MAX ? recent : INT_MAX);
-    p.need = (int32_t *)workspace;
-    p.g.plan = (int32_t *)((char *)workspace + up16(pages->rows * 4));
-    p.list = kept ? kept : (int32_t *)((char *)p.g.plan + up16(pages->rows * pages->max_pages * 4));
+    char *at = (char *)workspace;
+    auto part = [&](int64_t bytes) {
+        char *const x = at;
+        at += up16(bytes);
+        return x;
+    };
+    p.need = (int32_t *)part(pages->rows * 4);
+    p.len = (int32_t *)part(pages->rows * 4);
+    p.g.plan = (int32_t *)part(pages->rows * pages->max_pages * 4);
+    p.moved = (float *)part(pages->rows * max_len * 4);
+    p.moved_ld = max_len;
+    p.list = kept ? kept : (int32_t *)part(pages->rows * max_len * 4);
     p.list_ld = kept ? weights_ld : max_len;
     p.kinds = cache->k == cache->v ? 1 : 2;
     p.g.granted = granted;
@@ -1708,10 +1721,10 @@ DSEL_API dsel_status dsel_cache_evict(const dsel_pages *pages, const int32_t *bu
     g.arg = p.need;
     if ((st = launch((const void *)pool_give_kernel<kCut>, dim3(1), dim3(1024), &g, 0, stream)) != DSEL_OK) return st;
     const int64_t parts = p.kinds * cache->layers, runs = wgs_for((max_len + kEvictRows - 1) / kEvictRows, parts * pages->rows);
-    st = launch((const void *)evict_copy_kernel, dim3((unsigned)runs, (unsigned)parts, (unsigned)pages->rows), dim3(256), &p,
-                0, stream);
+    st = launch((const void *)evict_copy_kernel, dim3((unsigned)runs, (unsigned)parts + 1, (unsigned)pages->rows), dim3(256),
+                &p, 0, stream);
     if (st != DSEL_OK) return st;
-    return launch((const void *)evict_finish_kernel, dim3((unsigned)pages->rows), dim3(1024), &p, 0, stream);
+    return launch((const void *)evict_finish_kernel, dim3(1 + kEvictParts, (unsigned)pages->rows), dim3(1024), &p, 0, stream);
 }
 
 // ---- verify ----------------------------------------------------------------

@@ -73,6 +73,9 @@ constexpr int kJoinWords = 8;
 // 12.6; 8 rows of 17 nodes over 120 keys 13.8 against 16.3, over 250 18.0 against
 // 18.3.  (Other heads, other head sizes and 8-bit caches were not measured.)
 constexpr int kAttnWholeKeys = 256;
+// Under a window, whose keys begin inside a tile and come with a round of sinks, less
+// is split: 9 nodes under a window of 128 with 4 sinks 22.9 us whole, 14.9 split.
+constexpr int kWindowWholeKeys = 64;
 
 __device__ u32x4 g_attn_zero[1];  // what a key that is none reads (never written)
 

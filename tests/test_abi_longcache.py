@@ -79,7 +79,7 @@ def test_window_validation(lib):
     assert _window(lib, batch=0, **none) == 0 and _window(lib, batch=0, window=0, **none) == -1
     need = lambda B=2, T=9, Hq=32, H=8, D=128, dt=1, n=1 << 20, w=4096, s=4: \
         lib.dsel_tree_attn_window_workspace_bytes(B, T, Hq, H, D, dt, n, w, s)
-    assert need() > 0 and need(w=100) == 0 and need(n=64) == 0 and need(w=0) == 0 and need(s=-1) == 0 and need(dt=3) == 0
+    assert need() > 0 and need(w=50) == 0 and need(n=64) == 0 and need(w=0) == 0 and need(s=-1) == 0 and need(dt=3) == 0
     assert need(w=1 << 62, s=1 << 62) == need(w=1 << 20) > 0 and need(w=100, s=1 << 62) > 0 and need(dt=4) > 0
     wide = dict(table_ld=1 << 16, max_pages=1 << 16, window=4096)
     assert _window(lib, wsb=need() - 1, **wide) == -4 and _window(lib, ws=None, **wide) == -4
@@ -117,7 +117,7 @@ def test_evict_validation(lib):
     for kw in (dict(budget=F + 2), dict(w=F + 2), dict(g=F + 1), dict(kept=F + 1), dict(ws=F + 8), dict(refcount=F + 2)):
         assert evict(**kw) == -3, kw
     need = lib.dsel_cache_evict_workspace_bytes(3, 64, 16)
-    assert need == 16 + 48 + 768
+    assert need == 2 * 16 + 48 + 2 * 768
     assert evict(ws=None) == -4 and evict(b=need - 1) == -4
     assert evict(rows=0, table=None, budget=None, w=None, g=None, ws=None, b=0) == 0
     for bad in ((0, 64, 16), (4097, 64, 16), (3, 60, 16), (3, 0, 16), (3, 64, 0), (3, 1 << 31, 16)):
