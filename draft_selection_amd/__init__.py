@@ -848,9 +848,12 @@ def _blocks_on(dev, t, name, shape, sk):
         raise TypeError(f"{name} must be float8_e8m0fnu for a float4_e2m1fn_x2 cache")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if shape[-1] % 16 or t.shape != (*shape[:-1], shape[-1] // 16):
+    n = shape[-1] // 16
+    if shape[-1] % 16 or t.shape[:-1] != shape[:-1] or t.shape[-1] != n:
         raise ValueError(f"{name} must be [..., dim / 32], dim a multiple of 32")
-    if any(n > 1 and x != 16 * y for n, x, y in zip(shape[:-1], sk, t.stride())) or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    st = t.stride()
+    if [16 * x for x in st[:-1]] != list(sk[:-1]) and any(e > 1 and x != 16 * y for e, x, y in zip(shape[:-1], sk, st)) \
+            or (n > 1 and st[-1] != 1):
         raise ValueError(f"{name} must have the layout of its cache: a 16th of its strides, the last one 1")
     return t.data_ptr()
 

@@ -1592,11 +1592,15 @@ DSEL_API dsel_status dsel_pages_free(const dsel_pages *pages, const int32_t *whi
 
 namespace {
 
+template <CacheType F, int NK>
+const void *key_weights_of(int64_t dim) {
+    return dim <= 64    ? (const void *)key_weights_kernel<KeyWeightsCfg<F, 64, NK>>
+           : dim <= 128 ? (const void *)key_weights_kernel<KeyWeightsCfg<F, 128, NK>>
+                        : (const void *)key_weights_kernel<KeyWeightsCfg<F, 256, NK>>;
+}
 template <CacheType F>
-const void *key_weights_pick(int64_t dim) {
-    return dim <= 64    ? (const void *)key_weights_kernel<KeyWeightsCfg<F, 64>>
-           : dim <= 128 ? (const void *)key_weights_kernel<KeyWeightsCfg<F, 128>>
-                        : (const void *)key_weights_kernel<KeyWeightsCfg<F, 256>>;
+const void *key_weights_pick(int64_t dim, bool many) {
+    return many ? key_weights_of<F, 4>(dim) : key_weights_of<F, 1>(dim);
 }
 
 int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
@@ -1657,14 +1661,13 @@ DSEL_API dsel_status dsel_key_weights(const dsel_tree_attn_args *a, const dsel_c
     p.scale = a->scale;
     p.decay = decay;
     p.page_shift = page_shift_of(p.c.page_size);
-    const void *k = c.dt == DSEL_MXFP4  ? key_weights_pick<kMxfp4>(c.dim)
-                    : c.dt == DSEL_E4M3 ? key_weights_pick<kE4m3>(c.dim)
-                                        : key_weights_pick<kBf16>(c.dim);
-    // keys of their own for the waves where that still makes two workgroups a CU
-    const int64_t tiles = (max_len + 63) / 64;
-    const int most = c.heads >= 4 ? 4 : c.heads >= 2 ? 2 : 1;
-    p.hs = a->batch * tiles >= 4 * 2 * kAttnCUs ? 1 : most;
-    const int64_t keys = 4 / p.hs * 64, wgs = wgs_for((max_len + keys - 1) / keys, a->batch);
+    // 64 keys a wave, two waves to a head's keys, where that makes two workgroups a CU
+    const bool many = a->batch * ((max_len + 127) / 128) >= 2 * kAttnCUs;
+    p.hs = c.heads >= 4 && !many ? 4 : c.heads >= 2 ? 2 : 1;
+    const void *k = c.dt == DSEL_MXFP4  ? key_weights_pick<kMxfp4>(c.dim, many)
+                    : c.dt == DSEL_E4M3 ? key_weights_pick<kE4m3>(c.dim, many)
+                                        : key_weights_pick<kBf16>(c.dim, many);
+    const int64_t keys = 4 / p.hs * (many ? 64 : 16), wgs = wgs_for((max_len + keys - 1) / keys, a->batch);
     return launch(k, dim3((unsigned)wgs, (unsigned)a->batch), dim3(256), &p, 0, stream);
 }
 
