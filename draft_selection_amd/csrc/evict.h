@@ -47,7 +47,7 @@ constexpr int kEvictHeld = 16;
 __global__ __launch_bounds__(1024) void evict_plan_kernel(EvictParams p) {
     __shared__ int hist[32][256];
     __shared__ int part[17], bad;
-    __shared__ uint32_t found[2];
+    __shared__ uint32_t found[3];
     const int r = blockIdx.x, tid = threadIdx.x;
     int *const mine = hist[(tid >> 6) * 2 + (tid & 1)];
     const int K = p.budget[r], n = p.g.seq_len[r];
@@ -109,23 +109,32 @@ __global__ __launch_bounds__(1024) void evict_plan_kernel(EvictParams p) {
         }
         __syncthreads();
         int count = 0;
-        if (tid < 256)
-            for (int i = 0; i < 32; ++i) count += hist[i][255 - tid];  // from the largest digit down
+        if (tid < 256) {  // from the largest digit down
+#pragma unroll
+            for (int i = 0; i < 32; ++i) count += hist[i][255 - tid];
+        }
         int all;
         const int above = block_scan1024(count, part, &all);
         if (tid < 256 && above < m && above + count >= m) {
             found[0] = 255 - tid;
             found[1] = above;
+            found[2] = above + count == m;
         }
         if (tid == 0 && m == 0) {
             found[0] = 255;
-            found[1] = 0;
+            found[1] = found[2] = 0;
         }
         __syncthreads();
         key |= found[0] << shift;
         mask |= 255u << shift;
         m -= (int)found[1];
+        const bool all_kept = found[2] && key;
         __syncthreads();
+        if (all_kept) {  // every weight with these digits: no more are needed, and no ties
+            --key;
+            m = 0;
+            break;
+        }
     }
     // m of those that equal the key are kept, the first ones
     int32_t *list = p.list + r * p.list_ld;
