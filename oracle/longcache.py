@@ -17,7 +17,7 @@ def to_mxfp4(x):
     """Codes (one an element) and scale bytes of values ``[..., n]``, n a multiple of
     32.  The exponent is found by trying, the code by the distance to each value."""
     x = np.asarray(x, np.float64)
-    b = x.reshape(*x.shape[:-1], -1, 32)
+    b = x.reshape(*x.shape[:-1], x.shape[-1] // 32, 32)
     top = np.abs(b).max(-1)
     fine = np.isfinite(top)
     e = np.full(top.shape, 125)

@@ -338,3 +338,17 @@ def test_captured_weights_and_eviction(dev):
         torch.cuda.synchronize()
         for a, b in zip(state, got):
             assert torch.equal(a.view(torch.int16) if a.dtype is L.BF16 else a, b.view(torch.int16) if b.dtype is L.BF16 else b), i
+
+
+def test_evict_many_rows(dev):
+    """More rows than the pool's workgroup has threads."""
+    rng = np.random.default_rng(30)
+    seq = [int(x) for x in rng.integers(0, 13, 1300)]
+    budget = [int(x) for x in rng.integers(-1, 9, 1300)]
+    assert _evict(rng, dev, seq, budget, 4, 3, 1500, 0, 0, layers=1, H=1, D=8) == 1
+    assert ds.device_error() == 0
+
+
+def test_weights_of_many_rows(dev):
+    rng = np.random.default_rng(31)
+    _run(L.Case(rng, dev, 130, 2, 4, 2, 64, 16, rng.integers(0, 90, 130), L.FP4, "chain", lens=rng.integers(0, 3, 130)), 0.5)

@@ -103,3 +103,21 @@ def test_captured_and_replayed(dev):
         # bits: the last row comes to places that hold NaN
         assert torch.equal(got[0].view(torch.int16), out.view(torch.int16)), i
         assert torch.equal(got[1].view(torch.int32), lse.view(torch.int32)), i
+
+
+@pytest.mark.parametrize("dt", L.TYPES)
+def test_many_rows(dev, dt):
+    """More rows than a wave has lanes, each with a window of its own place."""
+    rng = np.random.default_rng(21)
+    L.Case(rng, dev, 150, 2, 4, 2, 64, 16, rng.integers(0, 400, 150), dt, "chain", lens=rng.integers(0, 3, 150)).run(70, 3)
+
+
+def test_a_window_over_a_mask_alone_and_depths_alone(dev):
+    """A mask without depths puts node i at i; depths without a mask leave the chain's visibility."""
+    c = L.Case(np.random.default_rng(22), dev, 2, 6, 2, 1, 64, 16, [40, 3], L.BF16, "tree")
+    depth, c.depth = c.depth, None
+    real, c.depth_np = c.depth_np, np.tile(np.arange(6), (2, 1))
+    c.run(3, 1)
+    c.depth, c.depth_np, c.mask = depth, real, None
+    c.vis = np.tile(np.tril(np.ones((6, 6), bool)), (2, 1, 1))
+    c.run(3, 1)
