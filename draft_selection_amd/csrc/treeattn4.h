@@ -97,6 +97,18 @@ struct Attn4Keys {
 };
 
 // ---- rows in tiles of 32 a wave ---------------------------------------------------
+//
+// Measured on an MI355X, caches in HBM, heads-first pages, 32 query heads on 8 of 128,
+// with the join: 64 chains of up to 17 nodes over up to 4,096 positions 121 us (283
+// TFLOP/s of products that count: 68 of the 128 rows of a tile do); 8 trees of up to
+// 64 over up to 16,384, 128 us; 2 of 32 over 131,000, 190 us (723, at 1.7 GHz: what the
+// card's power allows).  A round of 64 keys takes 3,900 cycles for the two waves of a
+// SIMD, of which the products are 2,048; the start, the parts of split tiles and the
+// join take some 35 us of every call.
+// On the way there: K straight to every row wave's registers (each widens the whole
+// tile) 131 and 207 us; products, softmax and widening after each other 131 and 209;
+// steps in one, but page ids fetched behind the vectors of a round (loads land in their
+// order, so each waited for all of them) 144 and 214.
 
 // DP: padded head dim; RW waves of 32 rows, each as CW waves that hold DP / CW
 // columns of the output, by KW key groups; KT keys a round
@@ -514,7 +526,10 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn4_kernel(TreeAttnPar
 
 // ---- at most 32 rows --------------------------------------------------------------
 
-// RR row tiles of 16; KW waves with 64 keys a round each
+// RR row tiles of 16; KW waves with 64 keys a round each.  Measured as above: one token
+// for each of 16 rows of up to 60,000 positions 132 to 150 us (5.1 to 4.5 TB/s; with
+// products of 32 rows 190), tokens-first pages 250 to 265; one token over 333
+// positions 11 us.
 template <bool WIN_, int DP_, int RR_, int KW_>
 struct Attn4FewCfg {
     static constexpr bool E4M3 = false, WIN = WIN_;
