@@ -408,6 +408,10 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn4_kernel(TreeAttnPar
         uint32_t seen = 0;  // what the lane's row sees of the 32 keys before
         Attn4Bits<C> lost;  // of the 32 keys that s is of
         lost.load(bits + 2 * C::VW, 0);
+        // The first round of one step widens K of r0 + 2 into the stage that these were
+        // read from, which every wave has to have done.  (Rounds of two steps widen into
+        // the other stage first, and meet before they come to this one.)
+        if constexpr (LAG) meet();
         // One step: scores s of 32 keys from position kb on, V of the 32 before in stage
         // VST, K of the 32 after in stage KST (sub-rounds VSUB and KSUB)
         auto step = [&](floatx16 &s, floatx16 &s2, int kb, auto vst, auto vsub, auto kst, auto ksub, auto side) {
