@@ -25,6 +25,11 @@ namespace dsel {
 // Scale byte s as 2^(s - 127); the conversions take its exponent alone, and 255 as NaN
 __device__ __forceinline__ float block_scale(uint32_t s) { return __uint_as_float(s << 23); }
 
+// Is a block of V to be kept out of the products?  255 is NaN, and under 253 and 254,
+// which no call writes, the larger codes pass bf16: 0 times those is no 0 either, and a
+// key that is none reads a slot that may hold anything.
+__device__ __forceinline__ bool not_finite(uint32_t s) { return s > 252; }
+
 // the 8 values of a word
 __device__ __forceinline__ bf16x8 widen_fp4(uint32_t w, float s) {
     const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
@@ -207,7 +212,7 @@ __device__ __forceinline__ float attn4_step(AttnState<C> &a, const floatx16 &s, 
 
 // A bit for each vector of 32 keys (vector i: key i / CH, columns 32 (i % CH) ..), as
 // the waves that widen them leave it in LDS: those of K whose page is none, those of
-// V that are NaN.  Both are rare, and are looked for after a step's products, when
+// V that are not finite.  Both are rare, and are looked for after a step's products, when
 // the words have long arrived.
 template <class C>
 struct Attn4Bits {
@@ -240,8 +245,8 @@ struct Attn4Bits {
         return r;
     }
 };
-// Blocks of V that are NaN enter the products as zeros; a row that sees the key of
-// one (bits of see) gets NaN in its columns.
+// Blocks of V that are not finite enter the products under a scale of 2^-127; a row that
+// sees the key of one (bits of see) gets NaN in its columns.
 template <class C>
 __device__ __forceinline__ void attn4_nan(AttnState<C> &a, const Attn4Bits<C> &nan, int nb0, uint32_t see) {
 #pragma unroll
@@ -350,7 +355,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn4_kernel(TreeAttnPar
             if (none(i)) return;
             const int rr = part(i) / C::CH, tn = C::turn(rr);
             if (j == 0) {
-                const bool nan = w.vs[i] == 255;
+                const bool nan = not_finite(w.vs[i]);
                 const uint64_t m = ballot(nan);
                 if (lane == 0) bits[st * C::VW + i * C::GW + gw] = m;
                 if (nan) w.vs[i] = 0;  // (what the block holds is still finite)
@@ -644,11 +649,11 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn4_few_kernel(TreeAtt
         int page = page_of(r0 + 1);
         for (int round = r0; round < r1; ++round) {
             // V into LDS (this wave's own), the scores of 64 keys, and the next loads
-            uint64_t nan = 0;  // lanes with a NaN block among V's: none, mostly
+            uint64_t nan = 0;  // lanes with a block among V's that is not finite: none, mostly
 #pragma unroll
             for (int i = 0; i < C::VC; ++i) {
                 const int part = i * 64 + lane, rr = part / C::CH, ch = part % C::CH, tn = C::turn(rr);
-                const bool is = vs[i] == 255;
+                const bool is = not_finite(vs[i]);
                 nan |= ballot(is);
                 const float f = block_scale(is ? 0 : vs[i]);
                 u32x4 w = v[i];
@@ -660,7 +665,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn4_few_kernel(TreeAtt
             uint32_t vbad[C::VC];
             if (nan) {
 #pragma unroll
-                for (int i = 0; i < C::VC; ++i) vbad[i] = vs[i] == 255;
+                for (int i = 0; i < C::VC; ++i) vbad[i] = not_finite(vs[i]);
             }
             floatx4 s[C::RR][4];
 #pragma unroll
@@ -744,7 +749,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn4_few_kernel(TreeAtt
                 }
             }
             if (nan) {
-                // NaN blocks of V entered as zeros: rows that see their keys get NaN there
+                // (as attn4_nan)
 #pragma unroll
                 for (int i = 0; i < C::VC; ++i)
                     for (uint64_t mm = ballot(vbad[i] != 0); mm; mm &= mm - 1) {
