@@ -39,6 +39,23 @@ inline bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
     return (uintptr_t)a < (uintptr_t)b + (uintptr_t)nb && (uintptr_t)b < (uintptr_t)a + (uintptr_t)na;
 }
 
+// `rows` runs of `width` bytes, `ld` from one to the next
+struct Span {
+    const void *at;  // NULL: no bytes
+    int64_t width, rows = 1, ld = 0;
+};
+// Do two of them share any bytes?  Runs may lie in each other's gaps.
+inline bool overlap(const Span &a, const Span &b) {
+    if (!a.at || !b.at || !overlap(a.at, (a.rows - 1) * a.ld + a.width, b.at, (b.rows - 1) * b.ld + b.width)) return false;
+    for (int64_t i = 0; i < a.rows; ++i) {
+        const int64_t lo = (int64_t)((uintptr_t)a.at - (uintptr_t)b.at) + i * a.ld;  // from b's begin on
+        // b's first run that ends behind lo
+        const int64_t j = lo < b.width ? 0 : b.rows > 1 ? (lo - b.width) / b.ld + 1 : 1;
+        if (j < b.rows && j * b.ld < lo + a.width) return true;
+    }
+    return false;
+}
+
 inline dsel_status launch(const void *kernel, dim3 grid, dim3 block, void *arg, size_t shmem,
                           dsel_stream_t stream) {
     void *args[] = {arg};
@@ -1694,10 +1711,19 @@ DSEL_API dsel_status dsel_cache_evict(const dsel_pages *pages, const int32_t *bu
     if (pages->rows == 0) return DSEL_OK;
     if (!weights || !granted) return DSEL_E_ARG;
     if (!aligned(weights, 4) || !aligned(kept, 4) || !aligned(granted, 4)) return DSEL_E_ALIGN;
-    if (!workspace || workspace_bytes < dsel_cache_evict_workspace_bytes(pages->rows, max_len, pages->page_size))
-        return DSEL_E_WORKSPACE;
+    const size_t need = dsel_cache_evict_workspace_bytes(pages->rows, max_len, pages->page_size);
+    if (!workspace || workspace_bytes < need) return DSEL_E_WORKSPACE;
     if (!aligned(workspace, 16)) return DSEL_E_ALIGN;
     if ((st = check_kv(cache, true)) != DSEL_OK) return st;
+    // one launch writes what others still read
+    const int64_t col = pages->rows * 4, ld = weights_ld * 4;
+    const Span all[] = {{weights, max_len * 4, pages->rows, ld}, {kept, max_len * 4, pages->rows, ld},
+                        {budget, col}, {granted, 4}, {workspace, (int64_t)need},
+                        {pages->table, pages->max_pages * 4, pages->rows, pages->table_ld * 4},
+                        {pages->row_pages, col}, {pages->seq_len, col}, {pages->refcount, pages->num_pages * 4}};
+    for (int i = 0; i < 5; ++i)
+        for (int j = i + 1; j < 9; ++j)
+            if (overlap(all[i], all[j])) return DSEL_E_ARG;
     p.budget = budget;
     p.weights = weights;
     p.ld = weights_ld;

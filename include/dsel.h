@@ -768,7 +768,10 @@ dsel_status dsel_key_weights(const dsel_tree_attn_args *args, const dsel_cache *
  *            before the move, in its first budget[r] entries (with granted 0, those
  *            that it would have kept); other entries are not written.
  *   workspace  dsel_cache_evict_workspace_bytes() bytes, 16-byte aligned; contents
- *              need no initialisation.  max_len = max_pages * page_size. */
+ *              need no initialisation.  max_len = max_pages * page_size.
+ * Requirements: weights, kept, budget, granted and the workspace share no memory
+ * with each other or with the pool's arrays (rows of one may lie in the gaps between
+ * those of another). */
 size_t dsel_cache_evict_workspace_bytes(int64_t rows, int64_t max_len, int64_t page_size);
 dsel_status dsel_cache_evict(const dsel_pages *pages, const int32_t *budget, float *weights, int64_t weights_ld,
                              int64_t sinks, int64_t recent, const dsel_cache *cache, int32_t *kept,
