@@ -246,6 +246,13 @@ struct AttnBatch {
     }
 };
 
+// May a node of a row of s cached positions see position k?  A page that is none is an
+// error there alone: rounds begin before the window and end behind the sinks.
+template <class C>
+__device__ __forceinline__ bool in_reach(const TreeAttnParams &p, int s, uint32_t k) {
+    return !C::WIN || (int)k < p.sinks || (int)k > s - p.window;
+}
+
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 
@@ -707,7 +714,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
         auto place = [&](int round, int page, uint64_t *ok) -> int64_t {
             const uint32_t k = key_pos(round);
             const bool in = k < (uint32_t)total, good = in && page >= 0 && page < p.c.num_pages;
-            if (in && !good) device_error(kErrPage);
+            if (in && !good && in_reach<C>(p, row.s, k)) device_error(kErrPage);
             const uint32_t slot = k - page_at(k) * (uint32_t)p.c.page_size;
             const int64_t off = 16 * ((int64_t)page * p.c.page_stride + (int64_t)slot * p.c.slot_stride);
             const uint64_t m = ballot(good);

@@ -324,8 +324,9 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn4_kernel(TreeAttnPar
 #pragma unroll
             for (int i = 0; i < C::VC; ++i) {
                 if (none(i)) break;
-                w.at[i] = keys.place(p, pos(round, i), w.page[i], &w.bad[i]) + min(part(i) % C::CH, last);
-                if (w.bad[i]) device_error(kErrPage);
+                const uint32_t k = pos(round, i);
+                w.at[i] = keys.place(p, k, w.page[i], &w.bad[i]) + min(part(i) % C::CH, last);
+                if (w.bad[i] && in_reach<C>(p, row.s, k)) device_error(kErrPage);
                 w.k[i] = ((const u32x4 *)p.c.k)[w.at[i]];
                 w.ks[i] = p.c.k_block[w.at[i]];
             }
@@ -640,7 +641,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn4_few_kernel(TreeAtt
             const uint32_t pos = (uint32_t)(first_key(round) + lane);
             bool bad;
             const int64_t off = keys.place(p, pos, page, &bad);
-            if (bad) device_error(kErrPage);
+            if (bad && in_reach<C>(p, row.s, pos)) device_error(kErrPage);
             *ok = ballot(pos < keys.total && !bad);
             return off;
         };

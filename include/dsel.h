@@ -614,7 +614,9 @@ dsel_status dsel_tree_attn(const dsel_tree_attn_args *args, const dsel_cache *ca
  *   depth   [batch, block] int32 as dsel_tree_mask writes it (values are held to
  *           0 .. block - 1); NULL: i (a chain).
  * Keys that no node sees are not read (beyond the 32 to 256 keys that are read
- * together).  Everything else is as for dsel_tree_attn; calls of the same window
+ * together), and their pages may be none: positions from `sinks` on and up to
+ * seq_len[b] - window set no DSEL_DEVERR_PAGE, so a server can have given pages
+ * back that lie wholly among them.  Everything else is as for dsel_tree_attn; calls of the same window
  * and sinks as well give the same bits.
  *   workspace  dsel_tree_attn_window_workspace_bytes() bytes, 16-byte aligned (may
  *              be NULL when that is 0). */
