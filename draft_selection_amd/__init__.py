@@ -740,8 +740,11 @@ _PACK_ATTN = struct.Struct("@P6qPPqqPPf4xPP").pack
 _PACK_PAGES = struct.Struct("@PqqqPPPqq").pack
 _PACK_STRIDES = struct.Struct("@4q").pack
 _I32, _F32, _BF16, _E4M3 = torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn
-_FP4, _E8M0 = torch.float4_e2m1fn_x2, torch.float8_e8m0fnu
-_CACHE_TYPES = {_BF16: BF16, _E4M3: E4M3, _FP4: MXFP4}
+# None in a torch without them: no cache is in 4 bits there, and nothing else asks for them
+_FP4, _E8M0 = getattr(torch, "float4_e2m1fn_x2", None), getattr(torch, "float8_e8m0fnu", None)
+_CACHE_TYPES = {_BF16: BF16, _E4M3: E4M3}
+if _FP4 is not None and _E8M0 is not None:
+    _CACHE_TYPES[_FP4] = MXFP4
 
 
 def _placed(fn):
