@@ -516,6 +516,11 @@ dsel_status dsel_dyn_conv(const uint16_t *x, const uint16_t *x_prev, const uint1
  * 1 <= dim <= DSEL_MAX_HEAD_DIM,
  * heads <= DSEL_MAX_HEADS, layers <= DSEL_MAX_LAYERS, page_size <=
  * DSEL_MAX_PAGE, max_pages * page_size < 2^31 - DSEL_MAX_PAGE. */
+#ifdef __GNUC__
+#define DSEL_UNNAMED __extension__ /* unnamed unions came into C in 2011 */
+#else
+#define DSEL_UNNAMED
+#endif
 typedef struct {
     void *k, *v;
     dsel_dtype dt;
@@ -524,15 +529,16 @@ typedef struct {
     int64_t page_size, slot_stride;
     int64_t heads, head_stride;
     int64_t dim;
-    union {
+    DSEL_UNNAMED union {
         const float *k_scale; /* E4M3: [layers, heads]; NULL = 1 */
         uint8_t *k_block;     /* MXFP4: one byte for 32 elements, never NULL */
     };
-    union {
+    DSEL_UNNAMED union {
         const float *v_scale;
         uint8_t *v_block;
     };
 } dsel_cache;
+#undef DSEL_UNNAMED
 
 /* tree_mask -- which nodes each node sees, and how deep it lies.
  *   mask   out [batch, block, ceil(block / 32)] int32: bit j % 32 of word j / 32
