@@ -1656,11 +1656,11 @@ DSEL_API dsel_status dsel_key_weights(const dsel_tree_attn_args *a, const dsel_c
     if (!aligned(a->q, 16) || !aligned(a->lse, 4) || !aligned(count, 4) || !aligned(weights, 4)) return DSEL_E_ALIGN;
     int64_t sq[3];
     if ((st = check_q(a, sq)) != DSEL_OK) return st;
-    const int64_t tokens = a->batch * a->block * 4, nw = ((a->batch - 1) * weights_ld + max_len) * 4;
-    if (overlap(weights, nw, a->lse, tokens * a->q_heads) || (count && overlap(weights, nw, count, tokens)) ||
-        overlap(weights, nw, a->seq_len, a->batch * 4) || (a->block_len && overlap(weights, nw, a->block_len, a->batch * 4)) ||
-        overlap(weights, nw, a->page_table, ((a->batch - 1) * a->table_ld + a->max_pages) * 4))
-        return DSEL_E_ARG;
+    const int64_t tokens = a->batch * a->block * 4, col = a->batch * 4;
+    const Span out = {weights, max_len * 4, a->batch, weights_ld * 4};
+    for (const Span &in : {Span{a->lse, tokens * a->q_heads}, Span{count, tokens}, Span{a->seq_len, col}, Span{a->block_len, col},
+                           Span{a->page_table, a->max_pages * 4, a->batch, a->table_ld * 4}})
+        if (overlap(out, in)) return DSEL_E_ARG;
     p.q = (const char *)a->q;
     p.sqb = sq[0];
     p.sqt = sq[1];
