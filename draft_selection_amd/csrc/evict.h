@@ -6,9 +6,11 @@
 // fresh pages, so a page that another row holds too is only read, and every row is
 // copied by as many workgroups as it takes, in no order.  The copy is bound by
 // memory and is nearly all of the time where there are many layers.  Measured on an
-// MI355X, 8 heads of 128 in bf16: 16 rows of 1,024 to 4,096 positions cut to 1,500 in
-// eight layers 279 us of copying (4.9 TB/s) and 32 of the rest; two rows of 550 and
-// 1,100 cut to 512 in one layer 28 us, of which the plan takes 11 and the pages 6.
+// MI355X, 8 heads of 128 in bf16, kernel by kernel: 16 rows of 1,024 to 4,096 positions
+// cut to 1,500 in eight layers 280 us of copying (4.9 TB/s), 15 the plan, 10 the pages, 5
+// the end; two rows of 550 and 1,100 cut to 512 in one layer 6, 9, 6 and 3.  Captured,
+// the four together: 312 and 28 us; two rows of 120,000 to 60,000 in one layer 461 (the
+// plan reads the weights of a row past 16,384 again in every pass).
 #pragma once
 
 #include "cache.h"

@@ -20,10 +20,10 @@
 // once, q once per 64 keys from the caches.  Pairs of waves share the heads of the
 // same keys.  Where that leaves CUs without work, a wave takes 16 keys and four
 // share the heads: latency counts then (lengths, page ids, keys, head by head).
-// Measured on an MI355X, 32 query heads on 8 of 128: one token over 700 positions 6.2
-// us (64 keys a wave: 14.5); 9 tokens for each of 32 rows of up to 8,192, 104 us (3.3
-// TB/s of K; 16 keys a wave: 135), in 4 bits 58; one token for each of 2 rows of up to
-// 131,000, 92 us (4.7 TB/s).
+// Measured on an MI355X, captured, 32 query heads on 8 of 128: one token over 700
+// positions 6.2 us (64 keys a wave: 14.5); 9 tokens for each of 32 rows of up to 8,192,
+// 104 us (3.3 TB/s of K; 16 keys a wave: 135), in 8 bits 77, in 4 bits 58; one token for
+// each of 2 rows of up to 131,000, 92 us (4.7 TB/s).
 #pragma once
 
 #include "treeattn4.h"

@@ -1678,7 +1678,9 @@ DSEL_API dsel_status dsel_key_weights(const dsel_tree_attn_args *a, const dsel_c
     p.scale = a->scale;
     p.decay = decay;
     p.page_shift = page_shift_of(p.c.page_size);
-    // 64 keys a wave, two waves to a head's keys, where that makes two workgroups a CU
+    // 64 keys a wave, two waves to a head's keys, where that makes two workgroups a CU.
+    // (By what the table holds: lengths are on the device.  One token over 700 positions
+    // takes 14.5 us instead of 6.2 where the table has room for 65,536 or more.)
     const bool many = a->batch * ((max_len + 127) / 128) >= 2 * kAttnCUs;
     p.hs = c.heads >= 4 && !many ? 4 : c.heads >= 2 ? 2 : 1;
     const void *k = c.dt == DSEL_MXFP4  ? key_weights_pick<kMxfp4>(c.dim, many)

@@ -74,7 +74,15 @@ constexpr int kJoinWords = 8;
 // 18.3.  (Other heads, other head sizes and 8-bit caches were not measured.)
 constexpr int kAttnWholeKeys = 256;
 // Under a window, whose keys begin inside a tile and come with a round of sinks, less
-// is split: 9 nodes under a window of 128 with 4 sinks 22.9 us whole, 14.9 split.
+// stays whole.  Captured, over 3,000 positions with 4 sinks, whole against split, in
+// bf16 / 8 bits / 4 bits, 32 query heads on 8 of 128: one token under a window of 60
+// 18.7 / 15.5 / 12.5 against 13.5 / 12.6 / 12.6 us, of 240 20.4 / 16.9 / 14.8 against
+// 13.7 / 12.8 / 12.6; 9 nodes under 60 20.1 / 19.0 / 20.1 against 14.9 / 14.9 / 16.0,
+// under 240 23.0 / 21.2 / 22.3 against 14.9 / 15.7 / 16.1.  8 rows of 9 nodes, heads
+// of 64, under 180: 15.6 / 14.3 / 18.5 against 13.8 / 12.4 / 15.4; 2 rows of 9, 16
+// heads on 4 of 256: 34.0 / 25.7 / 33.7 against 19.0 / 16.4 / 21.3.  Where every
+// workgroup has a tile, whole is the faster: 64 rows of 9 nodes under 180 28.3 / 26.6
+// / 27.5 against 30.4 / 29.1 / 29.9.
 constexpr int kWindowWholeKeys = 64;
 
 __device__ u32x4 g_attn_zero[1];  // what a key that is none reads (never written)
@@ -124,8 +132,8 @@ struct AttnCfg {
 //
 // Under a window the rounds are those that hold sinks and those from the first
 // position on that the root's window reaches; the rounds between are counted out,
-// so a row costs what its window costs, however long it is (64 chains of up to 17
-// nodes under 1,024: 80 us, 3.6 TB/s; 8 trees of up to 64 in 8 bits under 4,096: 82).
+// so a row costs what its window costs, however long it is (captured: 64 chains of up
+// to 17 nodes under 1,024 80 us, 3.6 TB/s; 8 trees of up to 64 in 8 bits under 4,096 82).
 struct AttnRow {
     int s, n;        // cached positions, nodes (0: nothing to do)
     int rts, rounds; // row tiles, rounds of each

@@ -103,11 +103,15 @@ struct Attn4Keys {
 
 // ---- rows in tiles of 32 a wave ---------------------------------------------------
 //
-// Measured on an MI355X, caches in HBM, heads-first pages, 32 query heads on 8 of 128,
-// with the join: 64 chains of up to 17 nodes over up to 4,096 positions 121 us (283
-// TFLOP/s of products that count: 68 of the 128 rows of a tile do); 8 trees of up to
-// 64 over up to 16,384, 128 us; 2 of 32 over 131,000, 190 us (723, at 1.7 GHz: what the
-// card's power allows).  A round of 64 keys takes 3,900 cycles for the two waves of a
+// Measured on an MI355X, captured, caches in HBM (three sets in turn), heads-first
+// pages, 32 query heads on 8 of 128, this kernel and the join together, medians: 64
+// chains of up to 17 nodes over up to 4,096 positions 121 us (283 TFLOP/s of products
+// that count: 68 of the 128 rows of a tile do); under a window of 1,024 67; 8 trees of
+// up to 64 over up to 16,384, 127 us; 32 chains of up to 9 over up to 2,048 44; 2 trees
+// of 32 over 131,000, 183 us (749, at 1.7 GHz: what the card's power allows).  16 heads
+// on 2 of 256, 16 trees of up to 21 over up to 5,000: 81 us (69 in a loop without the
+// step below, whose registers spill at that size: 184 to 204 bytes of a lane's; 24 to
+// 44 at 128, none at 64).  A round of 64 keys takes 3,900 cycles for the two waves of a
 // SIMD, of which the products are 2,048; the start, the parts of split tiles and the
 // join take some 35 us of every call.
 // On the way there: K straight to every row wave's registers (each widens the whole
@@ -537,9 +541,11 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn4_kernel(TreeAttnPar
 // ---- at most 32 rows --------------------------------------------------------------
 
 // RR row tiles of 16; KW waves with 64 keys a round each.  Measured as above: one token
-// for each of 16 rows of up to 60,000 positions 132 to 150 us (5.1 to 4.5 TB/s; with
-// products of 32 rows 190), tokens-first pages 250 to 265; one token over 333
-// positions 11 us.
+// for each of 16 rows of up to 60,000 positions 133 to 157 us (5.1 to 4.3 TB/s; with
+// products of 32 rows 190), tokens-first pages 256 to 265; one token over 333
+// positions 11 us.  Two row tiles, 8 tokens for each of 32 rows of 8,192: 160 us, and
+// 185 tokens-first; their registers spill (248 to 272 bytes of a lane's at 128, a
+// kilobyte at 256, where 8 tokens take 936 us and 2, in one tile, 135).
 template <bool WIN_, int DP_, int RR_, int KW_>
 struct Attn4FewCfg {
     static constexpr bool E4M3 = false, WIN = WIN_;
@@ -737,7 +743,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn4_few_kernel(TreeAtt
 #pragma unroll
                 for (int n = 0; n < C::RR; ++n)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[n][e] = (__bf16)s[n][2 * sub + (e >> 2)][e & 3];
+                    for (int e = 0; e < 8; ++e) w[n][e] = (__bf16)s[n][2 * sub + (e >> 2)][e & 3];  // (as attn_values)
 #pragma unroll
                 for (int nb = 0; nb < C::NB; ++nb) {
                     const char *const at = vt + vat[nb] + 32 * sub * C::RB;

@@ -39,7 +39,8 @@
  * array [batch] of int32 (4-byte aligned) giving block b's valid positions,
  * 0 <= block_len[b] <= block, in the same padded [batch, block] layout.  Block
  * b is then computed exactly as it would be alone at length block_len[b]
- * (same bits; dsel_tree_attn alone promises less, see there).  Outputs at padding positions (t >= block_len[b]) are not
+ * (same bits; dsel_tree_attn, dsel_tree_attn_window and dsel_key_weights promise
+ * less, see there).  Outputs at padding positions (t >= block_len[b]) are not
  * written, except where a call says so, and inputs there never affect a result
  * (they may hold anything, NaN included); a length outside [0, block] makes the
  * block empty and sets DSEL_DEVERR_BLOCK_LEN.  The launch geometry is that of
@@ -582,8 +583,8 @@ dsel_status dsel_tree_mask(const int32_t *parent, int64_t batch, int64_t block, 
  * get the bits that it gets alone.  It does, at the same block, where
  * dsel_tree_attn_workspace_bytes() is 0: no row is divided then.
  * Arithmetic: the products of q and K are exact bf16 products summed in fp32
- * (E4M3 values are exact in bf16, the scales are applied to the fp32 sums); the
- * softmax's maximum, weights and sum are fp32; the weights are rounded to bf16
+ * (E4M3 and MXFP4 values are exact in bf16, E4M3's scales are applied to the fp32
+ * sums); the softmax's maximum, weights and sum are fp32; the weights are rounded to bf16
  * for their products with V, which are summed in fp32.
  *   workspace  dsel_tree_attn_workspace_bytes() bytes, 16-byte aligned (may be
  *              NULL when that is 0); contents need no initialisation.  Calls that
@@ -622,8 +623,10 @@ dsel_status dsel_tree_attn(const dsel_tree_attn_args *args, const dsel_cache *ca
  * Keys that no node sees are not read (beyond the 32 to 256 keys that are read
  * together), and their pages may be none: positions from `sinks` on and up to
  * seq_len[b] - window set no DSEL_DEVERR_PAGE, so a server can have given pages
- * back that lie wholly among them.  Everything else is as for dsel_tree_attn; calls of the same window
- * and sinks as well give the same bits.
+ * back that lie wholly among them.  Positions are places in the cache: behind a
+ * dsel_cache_evict, which moves what it keeps together, the window reaches back by
+ * places, to tokens that were further away.  Everything else is as for
+ * dsel_tree_attn; calls of the same window and sinks as well give the same bits.
  *   workspace  dsel_tree_attn_window_workspace_bytes() bytes, 16-byte aligned (may
  *              be NULL when that is 0). */
 size_t dsel_tree_attn_window_workspace_bytes(int64_t batch, int64_t block, int64_t q_heads, int64_t kv_heads,
@@ -745,10 +748,12 @@ dsel_status dsel_pages_free(const dsel_pages *pages, const int32_t *which, dsel_
  *            weights_ld >= max_pages * page_size.
  * Positions at or past seq_len[b] are left as they are (so a new position starts
  * at the 0 it was cleared to), and so are positions whose page is none and rows
- * with no nodes.  A node and head whose lse is not finite, or whose count is not
- * above 0, counts nothing.  The cache's v and v_scale are not looked at.
+ * with no nodes (a row without a step has nothing decayed either).  A node and head
+ * whose lse is not finite, or whose count is not above 0, counts nothing.  The cache's v and v_scale are not looked at.
  * Arithmetic: bf16 products summed in fp32, the sums in fp32; each position is
- * summed by one workgroup in a fixed order, so calls repeat bit for bit.
+ * summed by one workgroup in a fixed order, so calls repeat bit for bit, and a row's
+ * sums do not depend on what other rows hold.  The order goes by the sizes (batch,
+ * heads, max_pages * page_size): in another batch or table the last bits may differ.
  * Requirements: cache->layers == 1 and cache->heads divides q_heads; q 16-byte
  * aligned, its strides multiples of 8; weights shares no memory with the inputs. */
 dsel_status dsel_key_weights(const dsel_tree_attn_args *args, const dsel_cache *cache, const float *count,
@@ -765,7 +770,9 @@ dsel_status dsel_key_weights(const dsel_tree_attn_args *args, const dsel_cache *
  * up to the old length.  All rows get their pages, or, when the pool is short, none
  * is cut: granted [1] int32 out is 1 or 0, and 0 sets DSEL_DEVERR_POOL.  (The old
  * pages are not free before the copies are made: cut some rows at a time where the
- * pool is nearly full.)
+ * pool is nearly full.)  From then on a position is a place in the row, no longer
+ * its token's number in the text: that, and the rotary position of the next token
+ * with it, is for the caller to keep.
  *   budget   [rows] int32: positions to keep; a row with budget[r] < 0 or >=
  *            seq_len[r] stays as it is.  So does one with budget[r] < sinks + recent
  *            or a length that its pages do not hold (DSEL_DEVERR_SEQ_LEN), or that
