@@ -716,8 +716,8 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn_kernel(TreeAttnPara
         };
         auto page_at = [&](uint32_t k) { return p.page_shift >= 0 ? k >> p.page_shift : k / (uint32_t)p.c.page_size; };
         auto entry_of = [&](int round) -> const int32_t * {
-            const uint32_t k = key_pos(round);
-            return table + (k < (uint32_t)total ? page_at(k) : 0u);
+            const uint32_t k = key_pos(round);  // (chosen, not branched on: as Attn4Keys::page)
+            return table + page_at(k < (uint32_t)total ? k : 0u);
         };
         auto place = [&](int round, int page, uint64_t *ok) -> int64_t {
             const uint32_t k = key_pos(round);

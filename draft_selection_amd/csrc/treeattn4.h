@@ -89,8 +89,11 @@ struct Attn4Keys {
     __device__ __forceinline__ uint32_t page_at(const TreeAttnParams &p, uint32_t k) const {
         return p.page_shift >= 0 ? k >> p.page_shift : k / (uint32_t)p.c.page_size;
     }
+    // (The position is chosen and not the lookup, so that no lanes branch around it: the
+    // compiler has put spills of all lanes at the join ahead of the mask's restore, and
+    // lanes past a row's end lost their scale bytes.)
     __device__ __forceinline__ int page(const TreeAttnParams &p, uint32_t pos) const {
-        return table[pos < total ? page_at(p, pos) : 0u];
+        return table[page_at(p, pos < total ? pos : 0u)];
     }
     __device__ __forceinline__ int64_t place(const TreeAttnParams &p, uint32_t pos, int page, bool *bad) const {
         const bool in = pos < total, good = in && (uint32_t)page < (uint32_t)p.c.num_pages;
