@@ -1337,8 +1337,9 @@ AttnKernels attn4_pick(int64_t rows, int64_t dim) {
                : rows <= 32 ? attn4_few_of<WIN, 128, 2, 4>()
                : rows <= 64 ? attn4_of<WIN, 128, 2, 1, 2, 32>()
                             : attn4_of<WIN, 128, 4, 1, 1, 64>();
+    // (Two row tiles of 256 columns do not fit the registers: a kilobyte of a lane's were
+    // kept in scratch, in the loop, and 8 tokens for each of 32 rows took 869 us, not 426.)
     return rows <= 16   ? attn4_few_of<WIN, 256, 1, 4>()
-           : rows <= 32 ? attn4_few_of<WIN, 256, 2, 4>()
            : rows <= 64 ? attn4_of<WIN, 256, 2, 2, 1, 32>()
                         : attn4_of<WIN, 256, 4, 2, 1, 32>();
 }

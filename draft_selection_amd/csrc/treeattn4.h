@@ -13,8 +13,9 @@
 // instructions, sooner than by memory, and there are two kernels:
 //   tree_attn4_kernel, rows in tiles of 32 a wave: the row waves of a key group widen
 //     a part of K's and V's tile each, for all of them;
-//   tree_attn4_few_kernel, at most 32 rows: a wave has keys of its own, K goes straight
-//     to registers, and products of 16 rows waste less of the matrix core and, what
+//   tree_attn4_few_kernel, at most 32 rows (16 of head sizes past 128, where two tiles
+//     of sums do not fit the registers): a wave has keys of its own, K goes straight to
+//     registers, and products of 16 rows waste less of the matrix core and, what
 //     counts more, half as many of the exponentials.
 #pragma once
 
@@ -113,8 +114,8 @@ struct Attn4Keys {
 // up to 64 over up to 16,384, 127 us; 32 chains of up to 9 over up to 2,048 44; 2 trees
 // of 32 over 131,000, 183 us (749, at 1.7 GHz: what the card's power allows).  16 heads
 // on 2 of 256, 16 trees of up to 21 over up to 5,000: 81 us (69 in a loop without the
-// step below, whose registers spill at that size: 184 to 204 bytes of a lane's; 24 to
-// 44 at 128, none at 64).  A round of 64 keys takes 3,900 cycles for the two waves of a
+// step below, whose registers spill at that size: 176 to 196 bytes of a lane's; 24 to
+// 36 at 128, none at 64).  A round of 64 keys takes 3,900 cycles for the two waves of a
 // SIMD, of which the products are 2,048; the start, the parts of split tiles and the
 // join take some 35 us of every call.
 // On the way there: K straight to every row wave's registers (each widens the whole
@@ -547,8 +548,8 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void tree_attn4_kernel(TreeAttnPar
 // for each of 16 rows of up to 60,000 positions 133 to 157 us (5.1 to 4.3 TB/s; with
 // products of 32 rows 190), tokens-first pages 256 to 265; one token over 333
 // positions 11 us.  Two row tiles, 8 tokens for each of 32 rows of 8,192: 160 us, and
-// 185 tokens-first; their registers spill (248 to 272 bytes of a lane's at 128, a
-// kilobyte at 256, where 8 tokens take 936 us and 2, in one tile, 135).
+// 185 tokens-first; their registers spill (248 to 268 bytes of a lane's at 128).  Head
+// size 256, one tile, 1 or 2 tokens: 136 us (4.2 TB/s).
 template <bool WIN_, int DP_, int RR_, int KW_>
 struct Attn4FewCfg {
     static constexpr bool E4M3 = false, WIN = WIN_;
